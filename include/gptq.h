@@ -396,6 +396,97 @@ int gptq_w4a16_gemm(float *Y, const uint16_t *X, const uint8_t *packed, const fl
                     const float *zeros, const int32_t *g_idx, int64_t M, int64_t N, int64_t K,
                     int group_size, int path, void *stream);
 
+/* Element types of the activations of the 8-bit calls below. */
+enum { GPTQ_BF16 = 0, GPTQ_F16 = 1, GPTQ_F32 = 2 };
+
+/*
+ * The 8-bit linear (W8A8): activations quantized a token at a time, weights a
+ * row at a time (gptq_quantize with bits = 8, group_size = -1), integer sums.
+ * Row pitches (ld*) are in elements.  An output does not overlap an input,
+ * but where a call says otherwise.  What lies between a row's end and its
+ * pitch is neither used nor written.
+ */
+
+/*
+ * Tokens to 8 bits, one scale a row: v = X or, with a gate, silu(gate) * X
+ * (the input of a gated MLP's down projection), in float32;
+ *     t = max_k |v_k|,  q_k = rint(127 v_k / t),  scale = t / 127,
+ *     sum = sum_k q_k,  hat_k = scale * q_k   (ties to even).
+ * Without a gate the codes are those of the exact quotients.  A row of zeros
+ * has codes 0 and scale 0; a row that holds an infinity or NaN has codes 0
+ * and scale NaN, so that what is computed from it is NaN.
+ *   Xq        int8 [M, K] OUT or NULL, pitch ldq a multiple of 16, 16-byte
+ *             aligned.
+ *   x_scales  float32 [M] OUT.
+ *   x_sums    int32 [M] OUT or NULL (the product needs it for weights with a
+ *             zero point).
+ *   hat       [M, K] OUT or NULL: the values the codes stand for, in X's
+ *             type (the input an 8-bit linear sees, for a calibration).
+ *             May be X itself (ldh = ldx).
+ *   X         [M, K] of `type`; gate the same, or NULL.
+ *   M >= 0 (0 is a no-op), 1 <= K <= 65536.  Xq or hat is given.
+ */
+int gptq_quantize_tokens(int8_t *Xq, int64_t ldq, float *x_scales, int32_t *x_sums, void *hat,
+                         int64_t ldh, const void *X, int64_t ldx, const void *gate, int64_t ldg,
+                         int type, int64_t M, int64_t K, void *stream);
+
+/*
+ * Between two blocks of a decoder layer: the norm after the block, its gate
+ * and residual scale, the residual sum, and the norm before the next block:
+ *     h' = block, or with post_norm: block * rsqrt(mean_k block^2 + eps) * post_weight
+ *     r' = residual + scale * gate * h'
+ *     out = r' * rsqrt(mean_k r'^2 + eps) * pre_weight
+ * in float32 from the inputs to the outputs: r' is rounded where it is
+ * stored, not before the second norm.  Means of squares are sums in float32
+ * (they overflow for rows of magnitude above about 1e19 / sqrt(D)).
+ *   stream_out  r' [M, D] OUT or NULL; may be residual itself (lds = ldr).
+ *   out         [M, D] OUT or NULL; may be block itself (ldo = ldb).
+ *   q           int8 [M, D] OUT or NULL: out as 8-bit tokens, quantized from
+ *               its float32 values (as gptq_quantize_tokens; same rules for
+ *               rows of zeros and rows that are not finite), with q_scales
+ *               float32 [M] and q_sums int32 [M] (or NULL).
+ *   block, residual  [M, D]; either may be NULL (then its term is 0), not both.
+ *   gate        [n_gates, D] or NULL (1): row m takes gate row m / gate_rows
+ *               (gate_rows >= 1; M for one gate of the whole batch).
+ *   post_weight, pre_weight  float32 [D] or NULL (1).
+ *   type        of block, residual, gate, stream_out and out.
+ *   M >= 0 (0 is a no-op), 1 <= D <= 65536; one output at least; eps >= 0.
+ */
+int gptq_block_norm(void *stream_out, int64_t lds, void *out, int64_t ldo, int8_t *q, int64_t ldq,
+                    float *q_scales, int32_t *q_sums, const void *block, int64_t ldb,
+                    const void *residual, int64_t ldr, const void *gate, int64_t ldg,
+                    int64_t gate_rows, const float *post_weight, const float *pre_weight,
+                    int post_norm, float scale, float eps, int type, int64_t M, int64_t D,
+                    void *stream);
+
+/*
+ * Lays the quantizer's 8-bit codes out for gptq_w8a8_gemm, once a layer:
+ *     Wq[n][k] = codes[n][k] - 128,  w_zeros[n] = zeros[n] - 128
+ * (s (q - z) is unchanged).  Wq int8 [N, K] at pitch ldw (a multiple of 16,
+ * >= K, 16-byte aligned), its padding written as 0; codes uint8 [N, K];
+ * zeros float32 [N], integers.  N >= 0, 1 <= K <= 65536.
+ */
+int gptq_w8a8_pack(int8_t *Wq, int64_t ldw, int32_t *w_zeros, const uint8_t *codes,
+                   const float *zeros, int64_t N, int64_t K, void *stream);
+
+/*
+ * Y[m][n] = x_scales[m] * w_scales[n] * sum_k Xq[m][k] (Wq[n][k] - w_zeros[n]) + bias[n].
+ * The integer sums are exact; the result is rounded to float32 once for the
+ * sum and once for each factor and the bias, then to Y's type.
+ *   Y         [M, N] OUT of y_type, pitch ldy.
+ *   Xq        int8 [M, K], pitch ldx; Wq int8 [N, K], pitch ldw: multiples of
+ *             16, 16-byte aligned.
+ *   x_scales  float32 [M];  w_scales float32 [N].
+ *   x_sums    int32 [M]: sum_k Xq[m][k]; read only with w_zeros.
+ *   w_zeros   int32 [N] in -128 .. 127, or NULL (symmetric weights).
+ *   bias      float32 [N] or NULL.
+ *   M, N >= 0 (0 is a no-op) up to 2^30, 1 <= K <= 65536, M N <= 2^40.
+ */
+int gptq_w8a8_gemm(void *Y, int64_t ldy, int y_type, const int8_t *Xq, int64_t ldx,
+                   const float *x_scales, const int32_t *x_sums, const int8_t *Wq, int64_t ldw,
+                   const float *w_scales, const int32_t *w_zeros, const float *bias, int64_t M,
+                   int64_t N, int64_t K, void *stream);
+
 /* dst[i] = (float) bf16 src[i] (exact widening), n >= 0 elements. */
 int gptq_bf16_to_f32(float *dst, const uint16_t *src, int64_t n, void *stream);
 

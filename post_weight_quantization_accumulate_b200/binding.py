@@ -47,8 +47,15 @@ SIGNATURES = [
     ("gptq_selftest_bounded_wait", _I, [_I64]),
     ("gptq_selftest_quotient", _I, [_I64, ctypes.c_uint64, _P]),
     ("gptq_w4a16_gemm", _I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P]),
+    ("gptq_quantize_tokens", _I, [_P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I, _I64, _I64, _P]),
+    ("gptq_block_norm", _I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _P,
+                             _P, _I, _F, _F, _I, _I64, _I64, _P]),
+    ("gptq_w8a8_pack", _I, [_P, _I64, _P, _P, _P, _I64, _I64, _P]),
+    ("gptq_w8a8_gemm", _I, [_P, _I64, _I, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _P]),
     ("gptq_bf16_to_f32", _I, [_P, _P, _I64, _P]),
 ]
+
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 W4A16_AUTO, W4A16_TENSOR_CORE, W4A16_GENERAL, W4A16_DECODE = 0, 1, 2, 3
 
@@ -314,6 +321,130 @@ def gptq_w4a16_gemm(Y: torch.Tensor, X: torch.Tensor, packed: torch.Tensor, scal
     _check("gptq_w4a16_gemm",
            lib().gptq_w4a16_gemm(_ptr(Y), _ptr(X), _ptr(packed), _ptr(scales), _ptr(zeros),
                                  _ptr(g_idx), M, N, K, group_size, path, _stream(Y, stream)))
+
+
+def _rows(t, dtype, shape, name):
+    """(address, row pitch) of a matrix whose rows are contiguous; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    # the pitch of a single row is not looked at: any that the library accepts
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else (shape[1] + 15) // 16 * 16
+
+
+def _vec(t, dtype, n, name):
+    """Address of a contiguous vector of n elements; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}]")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _type(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in TYPES:
+        raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor")
+    return TYPES[t.dtype]
+
+
+def _call_on(fn: str, t: torch.Tensor, others, stream, *args):
+    """Calls `fn` with the device of `t` current, on `stream` or that device's
+    current stream; every other tensor has to be on the same device."""
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError("tensor arguments must be on one device")
+    f = getattr(lib(), fn)
+    if not t.is_cuda or t.device.index == torch.cuda.current_device():
+        st = f(*args, _stream(t, stream))
+    else:
+        with torch.cuda.device(t.device):
+            st = f(*args, _stream(t, stream))
+    _check(fn, st)
+
+
+def gptq_quantize_tokens(Xq: torch.Tensor | None, x_scales: torch.Tensor, x_sums: torch.Tensor | None,
+                         X: torch.Tensor, gate: torch.Tensor | None = None,
+                         hat: torch.Tensor | None = None, stream=None):
+    """Xq (int8 [M, K], row pitch a multiple of 16), x_scales (float32 [M]),
+    x_sums (int32 [M]) and hat ([M, K], X's type) are outputs: the 8-bit
+    tokens of X, or of silu(gate) * X."""
+    ty = _type(X, "X")
+    M, K = X.shape
+    q, ldq = _rows(Xq, torch.int8, X.shape, "Xq")
+    h, ldh = _rows(hat, X.dtype, X.shape, "hat")
+    x, ldx = _rows(X, X.dtype, X.shape, "X")
+    g, ldg = _rows(gate, X.dtype, X.shape, "gate")
+    _call_on("gptq_quantize_tokens", X, (Xq, x_scales, x_sums, gate, hat), stream, q, ldq,
+             _vec(x_scales, torch.float32, M, "x_scales"), _vec(x_sums, torch.int32, M, "x_sums"), h, ldh,
+             x, ldx, g, ldg, ty, M, K)
+
+
+def gptq_block_norm(block: torch.Tensor | None, residual: torch.Tensor | None,
+                    pre_weight: torch.Tensor | None = None, *, stream_out: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                    q_scales: torch.Tensor | None = None, q_sums: torch.Tensor | None = None,
+                    post_norm: bool = False, post_weight: torch.Tensor | None = None,
+                    gate: torch.Tensor | None = None, gate_rows: int = 0, scale: float = 1.0,
+                    eps: float = 1e-6, stream=None):
+    """stream_out, out ([M, D], the inputs' type) and the tokens q (int8 [M,
+    D]), q_scales, q_sums are outputs; those not given are not computed."""
+    t = block if block is not None else residual
+    ty = _type(t, "block" if block is not None else "residual")
+    M, D = t.shape
+    so, lds = _rows(stream_out, t.dtype, t.shape, "stream_out")
+    o, ldo = _rows(out, t.dtype, t.shape, "out")
+    qp, ldq = _rows(q, torch.int8, t.shape, "q")
+    b, ldb = _rows(block, t.dtype, t.shape, "block")
+    r, ldr = _rows(residual, t.dtype, t.shape, "residual")
+    if gate is not None and gate_rows < 1:
+        raise ValueError("gate_rows must be positive")
+    g, ldg = _rows(gate, t.dtype, (-(-M // gate_rows) if gate is not None else 0, D), "gate")
+    _call_on("gptq_block_norm", t, (stream_out, out, q, q_scales, q_sums, block, residual, gate, post_weight,
+                                    pre_weight), stream, so, lds, o, ldo, qp, ldq,
+             _vec(q_scales, torch.float32, M, "q_scales"), _vec(q_sums, torch.int32, M, "q_sums"), b, ldb, r, ldr,
+             g, ldg, gate_rows, _vec(post_weight, torch.float32, D, "post_weight"),
+             _vec(pre_weight, torch.float32, D, "pre_weight"), int(bool(post_norm)), float(scale), float(eps),
+             ty, M, D)
+
+
+def gptq_w8a8_pack(Wq: torch.Tensor, w_zeros: torch.Tensor, codes: torch.Tensor, zeros: torch.Tensor, stream=None):
+    """Wq (int8 [N, K], row pitch a multiple of 16) and w_zeros (int32 [N])
+    from the quantizer's 8-bit codes (uint8 [N, K]) and zeros (float32 [N])."""
+    _need(codes, torch.uint8, "codes")
+    N, K = codes.shape
+    w, ldw = _rows(Wq, torch.int8, codes.shape, "Wq")
+    _call_on("gptq_w8a8_pack", codes, (Wq, w_zeros, zeros), stream, w, ldw, _vec(w_zeros, torch.int32, N, "w_zeros"),
+             _ptr(codes), _vec(zeros, torch.float32, N, "zeros"), N, K)
+
+
+def gptq_w8a8_gemm(Y: torch.Tensor, Xq: torch.Tensor, x_scales: torch.Tensor, Wq: torch.Tensor,
+                   w_scales: torch.Tensor, x_sums: torch.Tensor | None = None,
+                   w_zeros: torch.Tensor | None = None, bias: torch.Tensor | None = None, stream=None):
+    """Y [M, N] (bfloat16, float16 or float32) = the 8-bit tokens times the
+    8-bit weights transposed, scaled by row and column."""
+    ty = _type(Y, "Y")
+    _need(Xq, torch.int8, "Xq")
+    _need(Wq, torch.int8, "Wq")
+    M, K = Xq.shape
+    N = Wq.shape[0]
+    if w_zeros is not None and x_sums is None:
+        raise ValueError("weights with a zero point need x_sums")
+    y, ldy = _rows(Y, Y.dtype, (M, N), "Y")
+    x, ldx = _rows(Xq, torch.int8, (M, K), "Xq")
+    w, ldw = _rows(Wq, torch.int8, (N, K), "Wq")
+    _call_on("gptq_w8a8_gemm", Y, (Xq, x_scales, Wq, w_scales, x_sums, w_zeros, bias), stream, y, ldy, ty, x, ldx,
+             _vec(x_scales, torch.float32, M, "x_scales"), _vec(x_sums, torch.int32, M, "x_sums"), w, ldw,
+             _vec(w_scales, torch.float32, N, "w_scales"), _vec(w_zeros, torch.int32, N, "w_zeros"),
+             _vec(bias, torch.float32, N, "bias"), M, N, K)
 
 
 def gptq_bf16_to_f32(dst: torch.Tensor, src: torch.Tensor, stream=None):

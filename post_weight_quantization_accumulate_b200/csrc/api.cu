@@ -32,6 +32,13 @@ bool gemv_supported(const int32_t* g_idx, int64_t M, int64_t K, int gs);
 int run_w4a16(float* Y, const uint16_t* X, const uint8_t* packed, const float* scales,
               const float* zeros, const int32_t* g_idx, int64_t M, int64_t N, int64_t K, int gs,
               int path, cudaStream_t stream);
+int run_quantize_tokens(int8_t* Xq, int64_t ldq, float* x_scales, int32_t* x_sums, void* hat,
+                        int64_t ldh, const void* X, int64_t ldx, const void* gate, int64_t ldg,
+                        int type, int64_t M, int64_t K, cudaStream_t stream);
+int run_block_norm(const BlockNormArgs& a, int type, cudaStream_t stream);
+int run_w8a8_pack(int8_t* Wq, int64_t ldw, int32_t* w_zeros, const uint8_t* codes, const float* zeros,
+                  int64_t N, int64_t K, cudaStream_t stream);
+int run_w8a8(const W8A8Args& a, int y_type, cudaStream_t stream);
 int run_quantize_timed(float* W, const float* U, const int32_t* perm, int64_t d_out, int64_t d_in,
                        int bits, int gs, int block, uint8_t* codes, float* scales, float* zeros,
                        uint8_t* packed, int32_t* g_idx, float* err_sq, void* workspace,
@@ -51,6 +58,26 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 // Valid for 64-bit problem sizes that fit the kernels' 32-bit indexing.
 constexpr int64_t kMaxDim = 65536;
+
+// Rows of the 8-bit calls: counts fit 32-bit tile coordinates, pitches 64-bit
+// byte offsets.
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxPitch = int64_t(1) << 30;
+
+bool type_ok(int type) { return type == GPTQ_BF16 || type == GPTQ_F16 || type == GPTQ_F32; }
+
+// A matrix of `type` with rows of `cols` elements (NULL passes: the caller
+// decides what may be absent).
+bool rows_ok(const void* p, int64_t ld, int64_t cols, int type)
+{
+    return !p || (ld >= cols && ld <= kMaxPitch && aligned(p, type == GPTQ_F32 ? 4 : 2));
+}
+
+// Rows of 8-bit codes: tiled copies need 16-byte aligned rows.
+bool codes_ok(const void* p, int64_t ld, int64_t cols)
+{
+    return !p || (ld >= cols && ld <= kMaxPitch && ld % 16 == 0 && aligned(p, 16));
+}
 
 struct StreamPair {
     cudaStream_t copy = nullptr;
@@ -468,6 +495,81 @@ int gptq_quantize_q4k(float* W, const float* Hinv_chol, const int32_t* perm, int
     return run_quantize(W, Hinv_chol, perm, d_out, d_in, 4, 32, 128, codes, scales, offsets,
                         packed_int4, g_idx, err_sq, workspace, ws_bytes,
                         static_cast<cudaStream_t>(stream), true, &q4k);
+}
+
+int gptq_quantize_tokens(int8_t* Xq, int64_t ldq, float* x_scales, int32_t* x_sums, void* hat,
+                         int64_t ldh, const void* X, int64_t ldx, const void* gate, int64_t ldg,
+                         int type, int64_t M, int64_t K, void* stream)
+{
+    if (M < 0 || M > kMaxRows || K <= 0 || K > kMaxDim || !type_ok(type))
+        return GPTQ_ERR_INVALID_ARG;
+    if (!codes_ok(Xq, ldq, K) || !rows_ok(hat, ldh, K, type) || !rows_ok(X, ldx, K, type) ||
+        !rows_ok(gate, ldg, K, type))
+        return GPTQ_ERR_INVALID_ARG;
+    if (M == 0) return GPTQ_OK;
+    if (!X || (!Xq && !hat) || !x_scales || !aligned(x_scales, 4) || !aligned(x_sums, 4)) return GPTQ_ERR_INVALID_ARG;
+    int rc = check_device();
+    if (rc) return rc;
+    return run_quantize_tokens(Xq, ldq, x_scales, x_sums, hat, ldh, X, ldx, gate, ldg, type, M, K,
+                               static_cast<cudaStream_t>(stream));
+}
+
+int gptq_block_norm(void* stream_out, int64_t lds, void* out, int64_t ldo, int8_t* q, int64_t ldq,
+                    float* q_scales, int32_t* q_sums, const void* block, int64_t ldb,
+                    const void* residual, int64_t ldr, const void* gate, int64_t ldg,
+                    int64_t gate_rows, const float* post_weight, const float* pre_weight,
+                    int post_norm, float scale, float eps, int type, int64_t M, int64_t D,
+                    void* stream)
+{
+    if (M < 0 || M > kMaxRows || D <= 0 || D > kMaxDim || !type_ok(type) || !(eps >= 0.f) ||
+        (gate && gate_rows < 1))
+        return GPTQ_ERR_INVALID_ARG;
+    if (!codes_ok(q, ldq, D) || !rows_ok(stream_out, lds, D, type) || !rows_ok(out, ldo, D, type) ||
+        !rows_ok(block, ldb, D, type) || !rows_ok(residual, ldr, D, type) || !rows_ok(gate, ldg, D, type) ||
+        !aligned(post_weight, 4) || !aligned(pre_weight, 4))
+        return GPTQ_ERR_INVALID_ARG;
+    if (M == 0) return GPTQ_OK;
+    if ((!block && !residual) || (!stream_out && !out && !q) || (q && !q_scales) || !aligned(q_scales, 4) || !aligned(q_sums, 4))
+        return GPTQ_ERR_INVALID_ARG;
+    int rc = check_device();
+    if (rc) return rc;
+    return run_block_norm(BlockNormArgs{stream_out, lds, out, ldo, q, ldq, q_scales, q_sums, block, ldb,
+                                        residual, ldr, gate, ldg, gate_rows, post_weight, pre_weight,
+                                        post_norm, scale, eps, M, D},
+                          type, static_cast<cudaStream_t>(stream));
+}
+
+int gptq_w8a8_pack(int8_t* Wq, int64_t ldw, int32_t* w_zeros, const uint8_t* codes,
+                   const float* zeros, int64_t N, int64_t K, void* stream)
+{
+    if (N < 0 || N > kMaxRows || K <= 0 || K > kMaxDim || ldw < K || ldw > kMaxPitch) return GPTQ_ERR_INVALID_ARG;
+    if (N == 0) return GPTQ_OK;
+    if (!Wq || !w_zeros || !codes || !zeros || !codes_ok(Wq, ldw, K) || !aligned(w_zeros, 4) ||
+        !aligned(zeros, 4))
+        return GPTQ_ERR_INVALID_ARG;
+    int rc = check_device();
+    if (rc) return rc;
+    return run_w8a8_pack(Wq, ldw, w_zeros, codes, zeros, N, K, static_cast<cudaStream_t>(stream));
+}
+
+int gptq_w8a8_gemm(void* Y, int64_t ldy, int y_type, const int8_t* Xq, int64_t ldx,
+                   const float* x_scales, const int32_t* x_sums, const int8_t* Wq, int64_t ldw,
+                   const float* w_scales, const int32_t* w_zeros, const float* bias, int64_t M,
+                   int64_t N, int64_t K, void* stream)
+{
+    if (M < 0 || N < 0 || M > kMaxRows || N > kMaxRows || M * N > (int64_t(1) << 40) || K <= 0 ||
+        K > kMaxDim || !type_ok(y_type))
+        return GPTQ_ERR_INVALID_ARG;
+    if (!codes_ok(Xq, ldx, K) || !codes_ok(Wq, ldw, K) || !rows_ok(Y, ldy, N, y_type))
+        return GPTQ_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GPTQ_OK;
+    if (!Y || !Xq || !x_scales || !Wq || !w_scales || (w_zeros && !x_sums) || !aligned(x_scales, 4) ||
+        !aligned(x_sums, 4) || !aligned(w_scales, 4) || !aligned(w_zeros, 4) || !aligned(bias, 4))
+        return GPTQ_ERR_INVALID_ARG;
+    int rc = check_device();
+    if (rc) return rc;
+    return run_w8a8(W8A8Args{Y, ldy, Xq, ldx, x_scales, x_sums, Wq, ldw, w_scales, w_zeros, bias, M, N, K},
+                    y_type, static_cast<cudaStream_t>(stream));
 }
 
 int gptq_bf16_to_f32(float* dst, const uint16_t* src, int64_t n, void* stream)

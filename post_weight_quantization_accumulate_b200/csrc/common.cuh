@@ -78,6 +78,43 @@ struct Q4KOut {
     float* dmin;     // [d_out][d_in / 256] super-block scale of the mins
 };
 
+// Arguments of gptq_block_norm (csrc/tokens.cu) and gptq_w8a8_gemm (csrc/w8a8.cu).
+struct BlockNormArgs {
+    void* stream_out;
+    int64_t lds;
+    void* out;
+    int64_t ldo;
+    int8_t* q;
+    int64_t ldq;
+    float* q_scales;
+    int32_t* q_sums;
+    const void* block;
+    int64_t ldb;
+    const void* residual;
+    int64_t ldr;
+    const void* gate;
+    int64_t ldg, gate_rows;
+    const float* post_weight;
+    const float* pre_weight;
+    int post_norm;
+    float scale, eps;
+    int64_t M, D;
+};
+struct W8A8Args {
+    void* Y;
+    int64_t ldy;
+    const int8_t* Xq;
+    int64_t ldx;
+    const float* x_scales;
+    const int32_t* x_sums;
+    const int8_t* Wq;
+    int64_t ldw;
+    const float* w_scales;
+    const int32_t* w_zeros;
+    const float* bias;
+    int64_t M, N, K;
+};
+
 // Upper bound on one device-side wait, in SM clock cycles (about 1 s).
 constexpr long long kWaitLimitCycles = 2000000000LL;
 

@@ -20,6 +20,11 @@ with rms(x) = x / sqrt(mean_c x_c^2 + 1e-6) per token.  The products use the
 quantized weights rounded to bf16, fp32 accumulation and a bf16 result (the
 vendor bf16 GEMM through torch: glue between the calls, not a step of the
 GPTQ path); every GPTQ step runs in libgptq.so through `LayerQuantizer`.
+
+With `act_bits=8` the calibration is that of an 8-bit linear: each Hessian and
+each product sees the values that the inputs' 8-bit tokens stand for.
+`pack_w8a8` lays out what such a calibration gives (bits=8, group_size=-1) and
+`forward_w8a8` runs the layer with it, in 8-bit tokens and weights.
 """
 from __future__ import annotations
 
@@ -29,7 +34,7 @@ from dataclasses import dataclass, field
 import numpy as np
 import torch
 
-from . import synth
+from . import synth, w8a8
 from .layer import LayerQuantizer, QuantizedLayer
 
 GROUPS = (("qkv", ("q", "k", "v")), ("o", ("o",)), ("gate_up", ("gate", "up")), ("down", ("down",)))
@@ -82,16 +87,17 @@ def _rms(x: torch.Tensor) -> torch.Tensor:
     return (xf * torch.rsqrt(xf.pow(2).mean(dim=1, keepdim=True) + 1e-6)).to(torch.bfloat16)
 
 
-def next_inputs(group: str, inputs: dict, W_hat: dict) -> None:
+def next_inputs(group: str, inputs: dict, W_hat: dict, X: torch.Tensor | None = None) -> None:
     """The input of the group after `group`, from the quantized weights
-    (W_hat: bf16 [d_out, d_in] per linear); stored into `inputs`."""
+    (W_hat: bf16 [d_out, d_in] per linear); stored into `inputs`.  X is what
+    the group's linears read, where that is not inputs[group]."""
+    x = inputs[group] if X is None else X
     if group == "qkv":
-        inputs["o"] = _rms(inputs["qkv"] @ W_hat["v"].t())
+        inputs["o"] = _rms(x @ W_hat["v"].t())
     elif group == "o":
-        inputs["gate_up"] = _rms((inputs["qkv"].float() + (inputs["o"] @ W_hat["o"].t()).float())
+        inputs["gate_up"] = _rms((inputs["qkv"].float() + (x @ W_hat["o"].t()).float())
                                  .to(torch.bfloat16))
     elif group == "gate_up":
-        x = inputs["gate_up"]
         g = (x @ W_hat["gate"].t()).float()
         u = (x @ W_hat["up"].t()).float()
         inputs["down"] = (torch.nn.functional.silu(g) * u).to(torch.bfloat16)
@@ -115,18 +121,24 @@ def _copy(ql: QuantizedLayer) -> QuantizedLayer:
 
 def calibrate(X_attn: torch.Tensor, W: dict, shape: DecoderShape, bits: int = 4, group_size: int = 128,
               block_size: int = 128, damp: float = 0.01, act_order: bool = False,
-              keep_state: bool = False, cache: dict | None = None) -> DecoderResult:
+              keep_state: bool = False, cache: dict | None = None, act_bits: int = 16) -> DecoderResult:
     """Quantizes the seven linears group by group; each group's Hessian comes
-    from the input the earlier (already quantized) groups produce.
+    from the input the earlier (already quantized) groups produce.  With
+    act_bits=8 the linears read that input as 8-bit tokens (one scale a
+    token); `inputs` of the result holds it before that.
 
     `cache` (a dict the caller keeps between calls) holds the per-shape
     LayerQuantizer buffers, so that repeated calibrations of layers of the
     same shape reuse them -- and the library's CUDA graphs, which are keyed
     by the buffers' addresses -- instead of allocating and capturing anew."""
+    if act_bits not in (8, 16):
+        raise ValueError("act_bits is 8 or 16")
     res = DecoderResult()
     inputs = {"qkv": X_attn}
     for group, names in GROUPS:
         X = inputs[group]
+        if act_bits == 8:
+            X = w8a8.quantize_tokens(X, codes=False, hat=True).hat
         d_out, d_in = shape.linear_shape(names[0])
         key = (d_out, d_in, bits, group_size, block_size, damp, act_order, str(X.device))
         q = cache.get(key) if cache is not None else None
@@ -147,12 +159,31 @@ def calibrate(X_attn: torch.Tensor, W: dict, shape: DecoderShape, bits: int = 4,
         if keep_state:
             res.H[group], res.U[group], res.perm[group] = q.H.clone(), q.U.clone(), q.perm.clone()
         W_hat = {n: res.layers[n].W_hat.to(torch.bfloat16) for n in names}
-        next_inputs(group, inputs, W_hat)
+        next_inputs(group, inputs, W_hat, X)
         torch.cuda.synchronize()
         res.ms[group] = ev[0].elapsed_time(ev[1])
         del q
     res.inputs = inputs
     return res
+
+
+def pack_w8a8(layers: dict) -> dict:
+    """linear -> w8a8.Weight, from calibrated linears of 8 bits and one group
+    a row (DecoderResult.layers of calibrate(..., bits=8, group_size=-1))."""
+    return {name: w8a8.pack(layer) for name, layer in layers.items()}
+
+
+def forward_w8a8(X_attn: torch.Tensor, W: dict) -> torch.Tensor:
+    """The layer's output X_attn + attention + MLP for bf16 X_attn [n,
+    d_model], its linears (W: linear -> w8a8.Weight) in 8-bit tokens and
+    weights: the norms and the gated activation write 8-bit tokens, so no
+    activation but the residual stream and the products goes through memory
+    in more bits.  The mixing is that of the calibration (see above)."""
+    v = w8a8.linear(w8a8.quantize_tokens(X_attn), W["v"])
+    _, t = w8a8.block_norm(None, v, quantize=True, keep_stream=False)
+    x, t = w8a8.block_norm(w8a8.linear(t, W["o"]), X_attn, quantize=True)
+    t = w8a8.quantize_tokens(w8a8.linear(t, W["up"]), gate=w8a8.linear(t, W["gate"]))
+    return w8a8.block_norm(w8a8.linear(t, W["down"]), x, keep_out=False)[0]
 
 
 def quantized_weights(shape: DecoderShape) -> int:
