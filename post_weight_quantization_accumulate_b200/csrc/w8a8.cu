@@ -6,76 +6,542 @@
 // S[m] = sum_k x_q[m][k].  The integer sums are exact in 32 bits for K <=
 // 65536 (|x_q| <= 128, |w_q - z| <= 255: at most 2139095040 < 2^31), also
 // where the two terms of the difference are not: it is taken modulo 2^32.
-#include "common.cuh"
+// Integer sums have no order, so every variant gives the same bits.
+//
+// tcgen05 kind::i8 with the weights' rows as the M operand and the tokens as
+// the N operand: a tile's tokens can then be as few as 16, and a warp's 32
+// accumulator lanes are 32 neighbouring outputs of one token, so the results
+// go from registers to memory in whole sectors without a transpose, at any
+// pitch and alignment of Y.  Both operands are K-major rows of 128 codes
+// under the 128-byte swizzle; TMA fills what lies past K, M or N with zeros.
+//
+//  * pair kernel: 256 weight rows x NT tokens by a pair of CTAs (cta_group::2),
+//    persistent, double-buffered accumulators, so that the scaling and the
+//    stores of a tile overlap the products of the next.
+//  * split kernel: 128 weight rows x NT tokens by a cluster of CTAs that share
+//    K and add their partial sums through distributed shared memory: for few
+//    tokens, where the weights' way from memory is what counts and one tile a
+//    CTA would leave SMs without work.
+#include "pair.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <mutex>
 
 namespace gptq {
 
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kWords = 16;   // 4-code words of K per step
+constexpr int kRows = 128;      // weight rows of a CTA
+constexpr int kBK = 128;        // codes of K a stage
+constexpr int kStep = 32;       // codes of K an MMA
+constexpr int kWBytes = kRows * kBK;
 
 __device__ __forceinline__ void store_rounded(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_rounded(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_rounded(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The 4 codes k .. k+3 of a row, zero where k is past K.
-__device__ __forceinline__ int codes4(const int8_t* row, int k, int K)
+// Instruction descriptor of kind::i8: 32-bit integer sums of signed 8-bit
+// operands, both K-major.
+__host__ __device__ constexpr uint32_t idesc_i8(uint32_t M, uint32_t N)
 {
-    if (k >= K) return 0;
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(row + k);
-    return static_cast<int>(K - k >= 4 ? v : v & (0xffffffffu >> (8 * (4 - (K - k)))));
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// 64 x 64 outputs a block, 4 x 4 a thread, four products an instruction.
-template <typename T>
-__global__ void __launch_bounds__(256) w8a8_simt_kernel(W8A8Args a)
+template <int GROUP>
+__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
 {
-    __shared__ int xs[kWords][kTile + 1], ws[kWords][kTile + 1];
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int K = static_cast<int>(a.K);
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += 4 * kWords) {
-        for (int i = threadIdx.x; i < kTile * kWords; i += 256) {
-            const int r = i / kWords, w = i % kWords;
-            xs[w][r] = m0 + r < a.M ? codes4(a.Xq + (m0 + r) * a.ldx, k0 + 4 * w, K) : 0;
-            ws[w][r] = n0 + r < a.N ? codes4(a.Wq + (n0 + r) * a.ldw, k0 + 4 * w, K) : 0;
-        }
-        __syncthreads();
-        for (int w = 0; w < kWords; ++w)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(xs[w][ty + 16 * i], ws[w][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+    if constexpr (GROUP == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// The MMAs of one stage: `codes` codes of K from the rows at w and x.
+template <int GROUP>
+__device__ __forceinline__ void stage_mmas(uint32_t d, const uint8_t* w, const uint8_t* x, uint32_t idesc, int codes, bool first)
+{
+    const uint64_t wd = sdesc_sw128(smem_u32(w), 16, 1024);
+    const uint64_t xd = sdesc_sw128(smem_u32(x), 16, 1024);
+#pragma unroll
+    for (int k = 0; k < kBK / kStep; ++k)
+        if (k * kStep < codes)
+            umma_i8<GROUP>(d, wd + k * (kStep >> 4), xd + k * (kStep >> 4), idesc, first && k == 0 ? 0u : 1u);
+}
+
+// What the outputs of one weight row n share.
+struct RowScale {
+    float scale, bias;
+    uint32_t zero;
+};
+
+__device__ __forceinline__ RowScale row_scale(const W8A8Args& a, int64_t n)
+{
+    RowScale r{0.f, 0.f, 0u};
+    if (n < a.N) {
+        r.scale = a.w_scales[n];
+        if (a.bias) r.bias = a.bias[n];
+        if (a.w_zeros) r.zero = static_cast<uint32_t>(a.w_zeros[n]);
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m >= a.M || n >= a.N) continue;
-            uint32_t v = static_cast<uint32_t>(acc[i][j]);
-            if (a.w_zeros) v -= static_cast<uint32_t>(a.w_zeros[n]) * static_cast<uint32_t>(a.x_sums[m]);
-            const float y = static_cast<float>(static_cast<int>(v)) * a.w_scales[n] * a.x_scales[m];
-            store_rounded(static_cast<T*>(a.Y) + m * a.ldy + n, a.bias ? y + a.bias[n] : y);
+    return r;
+}
+
+// A token's scale and sum, as bits.
+__device__ __forceinline__ uint2 token_scale(const W8A8Args& a, int64_t m)
+{
+    if (m >= a.M) return make_uint2(0u, 0u);
+    return make_uint2(__float_as_uint(a.x_scales[m]), a.w_zeros ? static_cast<uint32_t>(a.x_sums[m]) : 0u);
+}
+
+__device__ __forceinline__ float output(int acc, const RowScale& r, uint2 t)
+{
+    const int sum = static_cast<int>(static_cast<uint32_t>(acc) - r.zero * t.y);
+    return __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(sum), r.scale), __uint_as_float(t.x)), r.bias);
+}
+
+// ------------------------------------------------------------- pair kernel
+constexpr int kPairThreads = 384;
+constexpr int kEpiWarps = 8;
+
+template <int NT>
+struct alignas(1024) PairSmem {
+    static constexpr int kXBytes = NT / 2 * kBK;    // this CTA's half of the tokens
+    static constexpr int kStageBytes = kWBytes + kXBytes;
+    static constexpr int kStages = 192 * 1024 / kStageBytes;
+    uint8_t stage[kStages][kStageBytes];
+    uint2 token[2][NT];
+    uint64_t full[kStages];    // first CTA: the bytes of both CTAs have landed
+    uint64_t empty[kStages];   // the MMAs have read the stage (both CTAs)
+    uint64_t tfull[2];         // tile complete (both CTAs)
+    uint64_t tempty[2];        // first CTA: both epilogues have read the accumulators
+    uint32_t tmem_base;
+    int abort;
+};
+
+// Tile number -> (weight tile, token tile).  Bands of kBand weight tiles,
+// walked token tile by token tile: the pairs that run at one time then cover
+// a compact block of tiles and share both operands in L2.
+constexpr int kBand = 8;
+__device__ __forceinline__ void tile_of(int t, int n_tiles, int m_tiles, int& tn, int& tm)
+{
+    const int band = t / (kBand * m_tiles);
+    const int width = min(kBand, n_tiles - band * kBand);
+    const int i = t - band * kBand * m_tiles;
+    tm = i / width;
+    tn = band * kBand + i % width;
+}
+
+template <int NT, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    w8a8_pair_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX, const W8A8Args a,
+                     int n_tiles, int m_tiles, int* status)
+{
+    using Smem = PairSmem<NT>;
+    constexpr int kStages = Smem::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster::cta_rank();
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const int K = static_cast<int>(a.K);
+    const int nk = (K + kBK - 1) / kBK;
+    const int tiles = n_tiles * m_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 1);
         }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&S.tfull[b], 1);
+            mbar_init(&S.tempty[b], 2 * kEpiWarps);
+        }
+        S.abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&mapW);
+        prefetch_tmap(&mapX);
+    }
+    if (warp == 1) {
+        cluster::pair_tmem_alloc(&S.tmem_base, 2 * NT);
+        cluster::pair_tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster::sync();   // both CTAs' barriers and tensor memory exist before any use
+    tc_fence_after();
+    const uint32_t tbase = S.tmem_base;
+    volatile int* abort = &S.abort;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += n_pairs) {
+                int tn, tm;
+                tile_of(t, n_tiles, m_tiles, tn, tm);
+                const int n0 = tn * 2 * kRows + static_cast<int>(rank) * kRows;
+                const int m0 = tm * NT + static_cast<int>(rank) * (NT / 2);
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (!mbar_wait_bounded(&S.empty[s], ((it / kStages) & 1) ^ 1, abort, status)) { ok = false; break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&S.full[s], 2 * Smem::kStageBytes);
+                    const uint32_t bar = cluster::map_address(&S.full[s], 0);
+                    cluster::pair_tma_load_2d(S.stage[s], &mapW, bar, k * kBK, n0);
+                    cluster::pair_tma_load_2d(S.stage[s] + kWBytes, &mapX, bar, k * kBK, m0);
+                }
+            }
+            // copies in flight land before the shared memory goes away: every
+            // one that was issued was waited for by the MMAs, unless a wait
+            // ran out; then the stages' own barriers are waited for here
+            int none = 0;
+            if (*abort && rank == 0)
+                for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                    mbar_wait_bounded(&S.full[i % kStages], (i / kStages) & 1, &none, nullptr, kWaitLimitCycles / 16);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            uint32_t it = 0, i = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += n_pairs, ++i) {
+                const int b = i & 1;
+                if (!mbar_wait_bounded(&S.tempty[b], ((i >> 1) & 1) ^ 1, abort, status)) break;
+                tc_fence_after();
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (!mbar_wait_bounded(&S.full[s], (it / kStages) & 1, abort, status)) { ok = false; break; }
+                    tc_fence_after();
+                    stage_mmas<2>(tbase + b * NT, S.stage[s], S.stage[s] + kWBytes, idesc_i8(2 * kRows, NT), K - k * kBK, k == 0);
+                    cluster::pair_commit(&S.empty[s]);
+                }
+                if (ok) cluster::pair_commit(&S.tfull[b]);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. +31, token half h
+        const int q = warp & 3;
+        const int h = (warp - 4) >> 2;
+        const int et = threadIdx.x - 128;
+        uint32_t i = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles; t += n_pairs, ++i) {
+            const int b = i & 1;
+            int tn, tm;
+            tile_of(t, n_tiles, m_tiles, tn, tm);
+            const int64_t n = static_cast<int64_t>(tn) * 2 * kRows + rank * kRows + q * 32 + lane;
+            const int64_t m0 = static_cast<int64_t>(tm) * NT;
+            // the buffer's readers, two tiles ago, are past the last barrier
+            if (et < NT) S.token[b][et] = token_scale(a, m0 + et);
+            const RowScale r = row_scale(a, n);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // after a wait that ran out every warp still takes part in the barriers of the tiles left
+            ok = ok && mbar_wait_warp(&S.tfull[b], (i >> 1) & 1, abort, status);
+            if (!ok) continue;
+            tc_fence_after();
+            const uint32_t taddr = tbase + (static_cast<uint32_t>(q * 32) << 16) + b * NT + h * (NT / 2);
+            T* y = static_cast<T*>(a.Y) + (m0 + h * (NT / 2)) * a.ldy + n;
+#pragma unroll 1
+            for (int c = 0; c < NT / 2; c += 32) {
+                float v[32];
+                tmem_ld_32x32b_x32(taddr + c, v);
+                tmem_ld_wait();
+                const int64_t left = a.M - (m0 + h * (NT / 2) + c);
+                if (n < a.N) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < left) {
+                            store_rounded(y, output(__float_as_int(v[j]), r, S.token[b][h * (NT / 2) + c + j]));
+                            y += a.ldy;
+                        }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) cluster::arrive_on(cluster::map_address(&S.tempty[b], 0));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster::sync();   // no MMA, commit or remote arrive of the pair is still in flight
+    if (warp == 1) {
+        tc_fence_after();
+        cluster::pair_tmem_dealloc(tbase, 2 * NT);
+    }
+}
+
+// ------------------------------------------------------------ split kernel
+constexpr int kSplitThreads = 192;   // loads, MMAs, four epilogue warps
+constexpr int kMaxStages = 12;
+constexpr int kMaxSplits = 8;
+
+struct SplitShared {
+    uint64_t full[kMaxStages], empty[kMaxStages], done;
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int NT, typename T>
+__global__ void __launch_bounds__(kSplitThreads)
+    w8a8_split_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX, const W8A8Args a,
+                      int splits, int stages, int* status)
+{
+    constexpr int kStageBytes = kWBytes + NT * kBK;
+    constexpr uint32_t kCols = NT < 32 ? 32 : NT;
+    __shared__ SplitShared S;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster::cta_rank());
+    const int n0 = static_cast<int>(blockIdx.x) / splits * kRows;   // a cluster is one tile
+    const int m0 = blockIdx.y * NT;
+    const int K = static_cast<int>(a.K);
+    const int blocks = (K + kBK - 1) / kBK;
+    const int k_begin = blocks * rank / splits, k_end = blocks * (rank + 1) / splits;
+    const int nk = k_end - k_begin;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 1);
+        }
+        mbar_init(&S.done, 1);
+        S.abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&mapW);
+        prefetch_tmap(&mapX);
+    }
+    if (warp == 1) {
+        tmem_alloc(&S.tmem_base, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = S.tmem_base;
+    volatile int* abort = &S.abort;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int k = 0;
+            for (; k < nk; ++k) {
+                const int s = k % stages;
+                if (!mbar_wait_bounded(&S.empty[s], ((k / stages) & 1) ^ 1, abort, status)) break;
+                uint8_t* st = base + s * kStageBytes;
+                mbar_arrive_expect_tx(&S.full[s], kStageBytes);
+                tma_load_2d(st, &mapW, &S.full[s], (k_begin + k) * kBK, n0);
+                tma_load_2d(st + kWBytes, &mapX, &S.full[s], (k_begin + k) * kBK, m0);
+            }
+            // after a wait that ran out: the copies issued land before the shared memory goes away
+            int none = 0;
+            if (*abort)
+                for (int i = max(0, k - stages); i < k; ++i)
+                    mbar_wait_bounded(&S.full[i % stages], (i / stages) & 1, &none, nullptr, kWaitLimitCycles / 16);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            for (int k = 0; k < nk; ++k) {
+                const int s = k % stages;
+                if (!mbar_wait_bounded(&S.full[s], (k / stages) & 1, abort, status)) { ok = false; break; }
+                tc_fence_after();
+                const uint8_t* st = base + s * kStageBytes;
+                stage_mmas<1>(tbase, st, st + kWBytes, idesc_i8(kRows, NT), K - (k_begin + k) * kBK, k == 0);
+                umma_commit(&S.empty[s]);
+            }
+            if (ok) umma_commit(&S.done);
+        }
+        __syncwarp();
+    } else {
+        // the partial sums to shared memory (the stages' place: they have
+        // been read), token by token; zeros where this CTA had no part of K
+        const int q = warp & 3;
+        int* part = reinterpret_cast<int*>(base);
+        const int row = q * 32 + lane;
+        if (nk == 0 || mbar_wait_warp(&S.done, 0, abort, status)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NT; c += 16) {
+                float v[16] = {};
+                if (nk > 0) {
+                    tmem_ld_32x32b_x16(tbase + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = __float_as_int(v[j]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster::sync();
+    {   // this CTA's share of the tile: 4 neighbouring outputs a thread
+        const int rows = static_cast<int>(min(static_cast<int64_t>(NT), a.M - m0));
+        const int quads = rows * (kRows / 4);
+        const int q0 = quads * rank / splits, q1 = quads * (rank + 1) / splits;
+        for (int e = q0 + static_cast<int>(threadIdx.x); e < q1; e += kSplitThreads) {
+            const int64_t m = m0 + e / (kRows / 4);
+            const int64_t n = n0 + 4 * (e % (kRows / 4));
+            if (n >= a.N) continue;
+            int sum[4] = {0, 0, 0, 0};
+            for (int p = 0; p < splits; ++p) {
+                const int4 v = cluster::load_int4(cluster::map_address(base + 16 * e, p));
+                sum[0] += v.x;
+                sum[1] += v.y;
+                sum[2] += v.z;
+                sum[3] += v.w;
+            }
+            const uint2 t = token_scale(a, m);
+            T* y = static_cast<T*>(a.Y) + m * a.ldy + n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < a.N) store_rounded(y + j, output(sum[j], row_scale(a, n + j), t));
+        }
+    }
+    cluster::sync();   // no CTA leaves while another reads its sums
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, kCols);
+    }
+}
+
+// ------------------------------------------------------------------- host
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// 8-bit rows in boxes of kBK codes x box_rows rows, 128-byte swizzle.
+int make_map(CUtensorMap* map, const int8_t* p, int64_t cols, int64_t rows, int64_t pitch, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail_msg("w8a8: tensor map encoding", cudaErrorInvalidValue);
+    return GPTQ_OK;
+}
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+int allow_smem(K kernel, int (&done)[64], int bytes)
+{
+    int dev = 0;
+    GPTQ_CUDA_CHECK(cudaGetDevice(&dev));
+    if (dev < 64 && done[dev] >= bytes) return GPTQ_OK;
+    GPTQ_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (dev < 64) done[dev] = bytes;
+    return GPTQ_OK;
+}
+
+template <int NT, typename T>
+int launch_pair(const W8A8Args& a, cudaStream_t stream)
+{
+    constexpr int smem = sizeof(PairSmem<NT>) + 1024;
+    static_assert(smem <= 227 * 1024, "one CTA per SM");
+    static int smem_set[64] = {};
+    int rc = allow_smem(w8a8_pair_kernel<NT, T>, smem_set, smem);
+    if (rc) return rc;
+    CUtensorMap mapW, mapX;
+    rc = make_map(&mapW, a.Wq, a.K, a.N, a.ldw, kRows);
+    if (rc) return rc;
+    rc = make_map(&mapX, a.Xq, a.K, a.M, a.ldx, NT / 2);
+    if (rc) return rc;
+    const int64_t n_tiles = (a.N + 2 * kRows - 1) / (2 * kRows), m_tiles = (a.M + NT - 1) / NT;
+    const int pairs = static_cast<int>(std::min<int64_t>(n_tiles * m_tiles, sm_count() / 2));
+    w8a8_pair_kernel<NT, T><<<2 * pairs, kPairThreads, smem, stream>>>(
+        mapW, mapX, a, static_cast<int>(n_tiles), static_cast<int>(m_tiles), device_status_ptr());
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+template <int NT, typename T>
+int launch_split(const W8A8Args& a, cudaStream_t stream)
+{
+    constexpr int stage_bytes = kWBytes + NT * kBK;
+    constexpr int max_stages = std::min(kMaxStages, 104 * 1024 / stage_bytes);   // two CTAs an SM
+    const int n_tiles = static_cast<int>((a.N + kRows - 1) / kRows), m_tiles = static_cast<int>((a.M + NT - 1) / NT);
+    const int blocks = static_cast<int>((a.K + kBK - 1) / kBK);
+    const int64_t tiles = static_cast<int64_t>(n_tiles) * m_tiles;
+    const int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({2 * sm_count() / tiles, kMaxSplits, blocks})));
+    const int stages = std::min(max_stages, (blocks + splits - 1) / splits);
+    const int smem = std::max(stages * stage_bytes, NT * kRows * 4) + 1024;
+    static int smem_set[64] = {};
+    int rc = allow_smem(w8a8_split_kernel<NT, T>, smem_set, smem);
+    if (rc) return rc;
+    CUtensorMap mapW, mapX;
+    rc = make_map(&mapW, a.Wq, a.K, a.N, a.ldw, kRows);
+    if (rc) return rc;
+    rc = make_map(&mapX, a.Xq, a.K, a.M, a.ldx, NT);
+    if (rc) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits * n_tiles, m_tiles);
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, w8a8_split_kernel<NT, T>, mapW, mapX, a, splits, stages, device_status_ptr());
+    if (e != cudaSuccess) return cuda_fail_msg("w8a8: cluster launch", e);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+template <typename T>
+int run_typed(const W8A8Args& a, cudaStream_t stream)
+{
+    if (a.M <= 16) return launch_split<16, T>(a, stream);
+    if (a.M <= 32) return launch_split<32, T>(a, stream);
+    if (a.M <= 64) return launch_split<64, T>(a, stream);
+    if (a.M <= 128) return launch_split<128, T>(a, stream);
+    return launch_pair<256, T>(a, stream);
 }
 
 }  // namespace
 
 int run_w8a8(const W8A8Args& a, int y_type, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>((a.M + kTile - 1) / kTile), static_cast<unsigned>((a.N + kTile - 1) / kTile));
-    if (y_type == GPTQ_F32)
-        w8a8_simt_kernel<float><<<grid, 256, 0, stream>>>(a);
-    else if (y_type == GPTQ_F16)
-        w8a8_simt_kernel<__half><<<grid, 256, 0, stream>>>(a);
-    else
-        w8a8_simt_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-    GPTQ_LAUNCH_CHECK();
-    return GPTQ_OK;
+    if (y_type == GPTQ_F32) return run_typed<float>(a, stream);
+    if (y_type == GPTQ_F16) return run_typed<__half>(a, stream);
+    return run_typed<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace gptq
