@@ -22,6 +22,12 @@
 //    K and add their partial sums through distributed shared memory: for few
 //    tokens, where the weights' way from memory is what counts and one tile a
 //    CTA would leave SMs without work.
+//  * few kernel (up to 16 tokens): 16 weight rows a block, the warps take turns
+//    along K and feed mma.sync straight from global loads.  Nothing but the
+//    weights' bytes counts there, and the set-up of tensor memory, barriers and
+//    clusters costs more than the products: 1 x 4096 x 4096 3.6 us against 7.9
+//    by the split kernel, 16 x 4096 x 11008 12.4 against 14.6, 32 x 4096 x
+//    11008 22.7 against 15.0 (the tokens' rows are read again by each block).
 #include "pair.cuh"
 
 #include <cuda_bf16.h>
@@ -420,6 +426,102 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
 }
 
+// -------------------------------------------------------------- few tokens
+// Lane (g, t) of a warp holds rows g and g + 8 of the weights and row g of the
+// tokens at 16 codes 16 t .. of each 64: two 8-code operands of two MMAs, the
+// same (permuted) order of K on both sides.  A row's 128 codes a step are read
+// in whole lines, U steps in flight a warp.
+constexpr int kFewWarps = 8;
+constexpr int kFewRows = 16;
+
+__device__ __forceinline__ uint4 load_once(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// The first `valid` of 16 codes, the others zero.
+__device__ __forceinline__ uint4 first_codes(uint4 v, int valid)
+{
+    if (valid >= 16) return v;
+    auto word = [valid](uint32_t w, int at) {
+        const int n = valid - at;
+        return n >= 4 ? w : n <= 0 ? 0u : w & (0xffffffffu >> (8 * (4 - n)));
+    };
+    return make_uint4(word(v.x, 0), word(v.y, 4), word(v.z, 8), word(v.w, 12));
+}
+
+// Sums of 16 weight rows x 8 tokens over 32 codes, signed.
+__device__ __forceinline__ void mma_i8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int MT, int U, typename T>
+__global__ void __launch_bounds__(kFewWarps * 32) w8a8_few_kernel(const W8A8Args a)
+{
+    __shared__ int part[kFewWarps][8 * MT][kFewRows];
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kFewRows;
+    const int K = static_cast<int>(a.K);
+    const int steps = (K + kBK - 1) / kBK;
+    // rows past the end repeat the last one; what they give is not stored
+    const int8_t* w0 = a.Wq + min(n0 + g, a.N - 1) * a.ldw;
+    const int8_t* w1 = a.Wq + min(n0 + g + 8, a.N - 1) * a.ldw;
+    const int8_t* x[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) x[j] = a.Xq + min(static_cast<int64_t>(8 * j + g), a.M - 1) * a.ldx;
+    int acc[MT][4] = {};
+    for (int s = warp; s < steps; s += kFewWarps * U) {
+        uint4 w[U][2][2], xb[U][2][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = (s + kFewWarps * u) * kBK + 64 * h + 16 * t;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                w[u][h][0] = k < K ? load_once(w0 + k) : zero;
+                w[u][h][1] = k < K ? load_once(w1 + k) : zero;
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    xb[u][h][j] = k < K ? first_codes(__ldg(reinterpret_cast<const uint4*>(x[j] + k)), K - k) : zero;
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    mma_i8(acc[j], w[u][h][0].x, w[u][h][1].x, w[u][h][0].y, w[u][h][1].y, xb[u][h][j].x, xb[u][h][j].y);
+                    mma_i8(acc[j], w[u][h][0].z, w[u][h][1].z, w[u][h][0].w, w[u][h][1].w, xb[u][h][j].z, xb[u][h][j].w);
+                }
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        part[warp][8 * j + 2 * t][g] = acc[j][0];
+        part[warp][8 * j + 2 * t + 1][g] = acc[j][1];
+        part[warp][8 * j + 2 * t][g + 8] = acc[j][2];
+        part[warp][8 * j + 2 * t + 1][g + 8] = acc[j][3];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 8 * MT * kFewRows; e += kFewWarps * 32) {
+        const int64_t m = e / kFewRows, n = n0 + e % kFewRows;
+        if (m >= a.M || n >= a.N) continue;
+        int sum = 0;
+#pragma unroll
+        for (int p = 0; p < kFewWarps; ++p) sum += part[p][m][e % kFewRows];
+        store_rounded(static_cast<T*>(a.Y) + m * a.ldy + n, output(sum, row_scale(a, n), token_scale(a, m)));
+    }
+}
+
 // ------------------------------------------------------------------- host
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -525,10 +627,20 @@ int launch_split(const W8A8Args& a, cudaStream_t stream)
     return GPTQ_OK;
 }
 
+template <int MT, int U, typename T>
+int launch_few(const W8A8Args& a, cudaStream_t stream)
+{
+    const unsigned blocks = static_cast<unsigned>((a.N + kFewRows - 1) / kFewRows);
+    w8a8_few_kernel<MT, U, T><<<blocks, kFewWarps * 32, 0, stream>>>(a);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
 template <typename T>
 int run_typed(const W8A8Args& a, cudaStream_t stream)
 {
-    if (a.M <= 16) return launch_split<16, T>(a, stream);
+    if (a.M <= 8) return launch_few<1, 4, T>(a, stream);
+    if (a.M <= 16) return launch_few<2, 2, T>(a, stream);
     if (a.M <= 32) return launch_split<32, T>(a, stream);
     if (a.M <= 64) return launch_split<64, T>(a, stream);
     if (a.M <= 128) return launch_split<128, T>(a, stream);
