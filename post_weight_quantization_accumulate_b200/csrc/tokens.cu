@@ -9,17 +9,27 @@
 //                    r' = r + scale g h';  out = r' rsqrt(mean r'^2 + eps)
 //                    w_pre, and its 8-bit tokens.
 //
-// One block per row, the row read once for each pass over it.
+// All of these are bound by memory: a row is read once, kept in registers
+// through its reductions and written once.  A row belongs to as many warps as
+// give each thread CH chunks of 16 bytes.  Chunks lie on 16-byte boundaries of
+// the row that is written; where its rows do not begin on one (an odd width),
+// a row's first and last chunk are partial, and what lies at other alignments
+// is read in two aligned pieces and shifted into place.  Element-wise accesses
+// instead cost about 90 instructions an element, with the issue slots and not
+// memory as the bound.
 #include "common.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace gptq {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kHeldCols = 16384;    // longest row kept in registers
+constexpr int kWideThreads = 1024;
 
 __device__ __forceinline__ float load_as_f32(const float* p) { return *p; }
 __device__ __forceinline__ float load_as_f32(const __half* p) { return __half2float(*p); }
@@ -28,158 +38,624 @@ __device__ __forceinline__ void store_rounded(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_rounded(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_rounded(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float silu(float a) { return a / (1.f + expf(-a)); }
-
-// Sum / unsigned maximum over the block; every thread gets the result.
-template <typename T, typename Op>
-__device__ __forceinline__ T block_reduce(T v, Op op)
+__device__ __forceinline__ void widen(uint32_t w, const __half*, float* v)
 {
-    __shared__ T part[kRowThreads / 32];
-    __syncthreads();
-    for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = part[0];
-    for (int i = 1; i < kRowThreads / 32; ++i) v = op(v, part[i]);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    v[0] = f.x;
+    v[1] = f.y;
+}
+__device__ __forceinline__ void widen(uint32_t w, const __nv_bfloat16*, float* v)
+{
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t narrow(float a, float b, const __half*)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t narrow(float a, float b, const __nv_bfloat16*)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---------------------------------------------------------------- chunks
+// 16 bytes of a row as they lie in memory, and how many elements that is.
+// Loads stand apart from what is computed with them: a thread's loads are all
+// on their way before the first is used.
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+
+// A row and a chunk of it: elements k .. k + kVec<T> - 1, of which those in
+// 0 .. K - 1 are there.  SHIFT: the row may begin off a 16-byte boundary (k
+// may then be negative, and the last chunk partial); else every chunk is whole.
+template <typename T>
+__device__ __forceinline__ bool whole(int k, int K) { return k >= 0 && k + kVec<T> <= K; }
+
+// Elements of a chunk that are not there become 0.
+template <typename T>
+__device__ __forceinline__ uint4 only_there(uint4 u, int k, int K)
+{
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            if (k + i < 0 || k + i >= K) w[i] = 0u;
+        } else {
+            if (k + 2 * i < 0 || k + 2 * i >= K) w[i] &= 0xffff0000u;
+            if (k + 2 * i + 1 < 0 || k + 2 * i + 1 >= K) w[i] &= 0x0000ffffu;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16 bytes at byte offset `o` (0 .. 15, a multiple of 2) of 32.
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o)
+{
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = (o & 8) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = (o & 4) ? w[i + 1] : w[i];
+    const int bits = 8 * (o & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The aligned 16 bytes at p, where one of them is between lo and hi: no byte
+// of another 16 is touched.
+__device__ __forceinline__ uint4 piece(uintptr_t p, uintptr_t lo, uintptr_t hi)
+{
+    return p + 16 > lo && p < hi ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <typename T, bool SHIFT>
+__device__ __forceinline__ uint4 load_chunk(const T* row, int k, int K, bool live)
+{
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (!SHIFT) {
+        return live && k < K ? *reinterpret_cast<const uint4*>(row + k) : zero;
+    } else {
+        if (!live || k >= K) return zero;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(row), hi = lo + K * sizeof(T);
+        const uintptr_t at = lo + static_cast<int64_t>(k) * static_cast<int64_t>(sizeof(T));
+        const int o = static_cast<int>(at & 15);
+        uint4 u = piece(at - o, lo, hi);
+        if (o) u = shifted(u, piece(at - o + 16, lo, hi), o);
+        return whole<T>(k, K) ? u : only_there<T>(u, k, K);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void widen_chunk(uint4 u, float (&v)[kVec<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        v[0] = __uint_as_float(u.x);
+        v[1] = __uint_as_float(u.y);
+        v[2] = __uint_as_float(u.z);
+        v[3] = __uint_as_float(u.w);
+    } else {
+        const T* t = nullptr;
+        widen(u.x, t, v);
+        widen(u.y, t, v + 2);
+        widen(u.z, t, v + 4);
+        widen(u.w, t, v + 6);
+    }
+}
+
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void store_chunk(T* row, int k, int K, const float (&v)[kVec<T>])
+{
+    if (!SHIFT || (whole<T>(k, K) && reinterpret_cast<uintptr_t>(row + k) % 16 == 0)) {
+        uint4 u;
+        if constexpr (sizeof(T) == 4)
+            u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else
+            u = make_uint4(narrow(v[0], v[1], row), narrow(v[2], v[3], row), narrow(v[4], v[5], row), narrow(v[6], v[7], row));
+        *reinterpret_cast<uint4*>(row + k) = u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec<T>; ++j)
+            if (k + j >= 0 && k + j < K) store_rounded(row + k + j, v[j]);
+    }
+}
+
+// v *= the float32 weights of the chunk's elements.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ void times_weights(float (&v)[VEC], const float* w, int k, int K)
+{
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+        const uint4 u = load_chunk<float, SHIFT>(w, k + i, K, true);
+        v[i] *= __uint_as_float(u.x);
+        v[i + 1] *= __uint_as_float(u.y);
+        v[i + 2] *= __uint_as_float(u.z);
+        v[i + 3] *= __uint_as_float(u.w);
+    }
+}
+
+// Elements of the row before the first 16-byte boundary's chunk: chunk c is
+// at k = kVec c - lead.
+template <typename T>
+__device__ __forceinline__ int lead_of(const void* row)
+{
+    return static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+}
+
+// ------------------------------------------------------------- reductions
+// expf is good to 2 steps, the reciprocal and its product to 2 more; for a
+// far below 0 the reciprocal of an infinite sum is 0.
+__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.f + expf(-a)); }
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-struct Add {
-    template <typename T>
-    __device__ T operator()(T a, T b) const { return a + b; }
-};
-struct Max {
-    __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
-};
+// Over the `warps` warps of a row, the block's row-th.  Each reduction of a
+// kernel has slots of its own, so that one barrier each is enough.
+__device__ __forceinline__ float row_sum(float v, float (&part)[32], int row, int warps, int warp)
+{
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[row * warps + warp] = v;
+    __syncthreads();
+    return warp_sum(lane < warps ? part[row * warps + lane] : 0.f);
+}
 
-// The grid of one row from t = max |v|, given as the bits of t (as unsigned
-// integers the magnitudes' bits keep their order, with infinities and then
-// NaN above every finite value).
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (&part)[32], int row, int warps, int warp)
+{
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[row * warps + warp] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, lane < warps ? part[row * warps + lane] : 0u);
+}
+
+// The sum ends up with the row's first warp.
+__device__ __forceinline__ int row_sum_first(int v, int (&part)[32], int row, int warps, int warp)
+{
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[row * warps + warp] = v;
+    __syncthreads();
+    return warp == 0 ? __reduce_add_sync(0xffffffffu, lane < warps ? part[row * warps + lane] : 0) : 0;
+}
+
+// ------------------------------------------------------------------ codes
+// A row's codes: q = rint(127 v / t), t = max |v|.
+//
+// One multiply-add: rint(v r), r = 127 / t rounded up, by adding kRound (1.5 *
+// 2^23): the sum's only rounding is to a whole number, and a code's two's
+// complement is its low byte.  Where t is so small or large that r would leave
+// the normal numbers, v and t are taken times c = 2^+-100 first.
+//
+// This gives the exact codes of values of 8 or 11 significant bits: a quotient
+// below 2^(8-p) that is no tie lies 2^-(12+p) or more from one, and v r within
+// 2^-(15+p) of the quotient.  Of a tie, 254 v / t is an odd number; 127 being a
+// prime, t's odd part then is a multiple of 127 or 2 |v| = t.  In the second
+// case the tie is 63.5, and r being no less than 127 / t it goes to 64, as it
+// should.  In the first r is a power of two and v r exact if the odd part is
+// 127 itself; rows of other multiples (11 bits: 7 of 1024 significands) divide:
+// the product with the rounded reciprocal of t and one correction step give
+// the quotient of 127 v (18 bits, exact) and t rounded to nearest (Markstein;
+// the exception, a divisor whose significand is all ones, has 24 bits), and a
+// tie is representable.
+//
+// Values of 24 bits (EXACT): a quotient within 2^-13 of a tie h is decided by
+// the sign of 254 v - 2 h t: the product 254 v in two parts, 2 h t from the
+// first part without a rounding, since the two are so near.
+constexpr float kRound = 12582912.f;
+
+enum CodeKind { kZeros, kMultiply, kDivide };
+
 struct TokenGrid {
-    float scale;   // t / 127; 0 for a row of zeros, NaN for a row with an infinite or NaN value
-    float c127;    // 127 c, c = 2^+-100 where t is so small or large that 127 v or 1 / t would leave fp32's range
-    float b;       // c t
-    float rb;      // 1 / b
-    float top;     // t
-    bool ok;       // codes are not all 0
+    CodeKind kind;   // kZeros: a row of zeros, or one that holds an infinity or NaN
+    float scale;     // t / 127; NaN for a row that is not finite
+    float c, t, r;   // 2^0 or 2^+-100; c times the maximum; 127 / t rounded up
 };
 
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The row's maximum is given by its bits: as unsigned integers the magnitudes'
+// bits keep their order, with infinities and then NaN above every finite value.
+template <bool ELEVEN>
 __device__ __forceinline__ TokenGrid token_grid(uint32_t top_bits)
 {
     TokenGrid g;
-    g.top = __uint_as_float(top_bits);
-    g.ok = top_bits != 0 && top_bits < 0x7f800000u;
-    g.scale = top_bits < 0x7f800000u ? __fdiv_rn(g.top, 127.f) : __uint_as_float(0x7fffffffu);
-    const float c = g.top < 0x1p-100f ? 0x1p100f : g.top > 0x1p100f ? 0x1p-100f : 1.f;
-    g.c127 = 127.f * c;
-    g.b = g.top * c;
-    g.rb = __frcp_rn(g.b);
+    const float top = __uint_as_float(top_bits);
+    const bool finite = top_bits < 0x7f800000u;
+    g.scale = finite ? __fdiv_rn(top, 127.f) : __uint_as_float(0x7fffffffu);
+    g.c = top < 0x1p-100f ? 0x1p100f : top > 0x1p100f ? 0x1p-100f : 1.f;
+    g.t = top * g.c;
+    g.r = __fdiv_ru(127.f, g.t);
+    const bool ties = ELEVEN && (((top_bits & 0x7fffffu) | 0x800000u) >> 13) % 127u == 0u;
+    g.kind = top_bits == 0u || !finite ? kZeros : ties ? kDivide : kMultiply;
     return g;
 }
 
-// rint(127 v / t).  One correction step on the product with the rounded
-// reciprocal gives the quotient of (127 c v) / (c t) rounded to nearest
-// (Markstein; the exception, a divisor whose significand is all ones, has 24
-// significant bits).  For v and t of at most 11 significant bits 127 v is
-// exact, a quotient that is no tie lies at least 2^-19 (relative) from one
-// and a tie is representable, so the code is the exact one.  EXACT (v of 24
-// bits): the quotient is within 127 * 2^-22 of 127 v / t, and one that near
-// to a tie is decided in double (127 v is exact there, and a quotient that is
-// no tie lies 2^-33 from one).
-template <bool EXACT>
-__device__ __forceinline__ int token_code(float v, const TokenGrid& g)
+// kRound + the code of v, whose quotient is next to a tie: c is one side's.
+__device__ __forceinline__ float beside_tie(float v, float c, const TokenGrid& g)
 {
-    const float a = v * g.c127;
-    const float t0 = a * g.rb;
-    const float t = fmaf(fmaf(-t0, g.b, a), g.rb, t0);
-    const float q = rintf(t);
-    if (EXACT && fabsf(fabsf(t - q) - 0.5f) < 1e-4f)
-        return static_cast<int>(rint(127.0 * static_cast<double>(v) / static_cast<double>(g.top)));
-    return static_cast<int>(q);
+    const float q = c - kRound;
+    const float side = copysignf(1.f, fmaf(v, g.r, -q));
+    const float h2 = 2.f * q + side;
+    const float p = 254.f * v;
+    const float d = fmaf(-h2, g.t, p) + fmaf(254.f, v, -p);
+    // over the tie, or on it and q odd
+    const bool over = d * side > 0.f || (d == 0.f && (static_cast<int>(q) & 1));
+    return over ? c + side : c;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-    quantize_tokens_kernel(int8_t* Xq, int64_t ldq, float* x_scales, int32_t* x_sums, T* hat,
-                           int64_t ldh, const T* X, int64_t ldx, const T* gate, int64_t ldg, int K)
+// v becomes kRound + its code.
+template <int VEC, bool ELEVEN, bool EXACT>
+__device__ __forceinline__ void code_chunk(float (&v)[VEC], const TokenGrid& g)
 {
+    if (g.kind == kZeros) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = kRound;
+        return;
+    }
+    if (g.c != 1.f) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] *= g.c;
+    }
+    if (ELEVEN && g.kind == kDivide) {
+        const float rt = __frcp_rn(g.t);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const float a = 127.f * v[j], q = a * rt;
+            v[j] = kRound + fmaf(fmaf(-q, g.t, a), rt, q);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        const float c = fmaf(v[j], g.r, kRound);
+        if (EXACT && fabsf(fmaf(v[j], g.r, kRound - c)) > 0.5f - 0x1p-13f)
+            v[j] = beside_tie(v[j], c, g);
+        else
+            v[j] = c;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack4(const float* v)
+{
+    return __byte_perm(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040),
+                       __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040), 0x5410);
+}
+
+// Stores the codes of the chunk at k (elements not there have code 0) and
+// returns their sum.  Called by whole warps, whose lanes hold neighbouring
+// chunks.  Off the boundaries of the codes' row a lane stores the word that
+// its chunk shares with the next lane's; at the warp's ends, and at the row's,
+// single codes.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live, const float (&v)[VEC])
+{
+    uint32_t w[VEC / 4];
+    int sum = 0;
+#pragma unroll
+    for (int j = 0; j < VEC / 4; ++j) {
+        w[j] = pack4(v + 4 * j);
+        sum = __dp4a(static_cast<int>(w[j]), 0x01010101, sum);
+    }
+    if (!row) return sum;
+    const uint64_t own = VEC == 8 ? static_cast<uint64_t>(w[VEC / 4 - 1]) << 32 | w[0] : w[0];
+    auto put = [&](uint64_t codes, int at, int from, int to) {   // codes[from .. to) at row[at + from ..)
+        if (from == 0 && to == VEC && at >= 0 && at + VEC <= K) {
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint64_t*>(row + at) = codes;
+            else
+                *reinterpret_cast<uint32_t*>(row + at) = static_cast<uint32_t>(codes);
+        } else {
+            for (int j = from; j < to; ++j)
+                if (at + j >= 0 && at + j < K) row[at + j] = static_cast<int8_t>(codes >> (8 * j));
+        }
+    };
+    if constexpr (!SHIFT) {
+        if (live && k < K) put(own, k, 0, VEC);
+    } else {
+        const int lead = (VEC - k % VEC) % VEC;   // codes that belong to the word before; the same for a whole row
+        uint64_t next = 0;
+        if (lead) next = __shfl_down_sync(0xffffffffu, own, 1);
+        if (live && k < K) {
+            const int lane = threadIdx.x & 31;
+            if (lead && lane == 0) put(own << (8 * (VEC - lead)), k + lead - VEC, VEC - lead, VEC);
+            const uint64_t word = lead ? own >> (8 * lead) | next << (8 * (VEC - lead)) : own;
+            put(word, k + lead, 0, lead && lane == 31 ? VEC - lead : VEC);
+        }
+    }
+    return sum;
+}
+
+// ---------------------------------------------------------------- kernels
+struct TokenArgs {
+    int8_t* Xq;
+    int64_t ldq;
+    float* x_scales;
+    int32_t* x_sums;
+    void* hat;
+    int64_t ldh;
+    const void* X;
+    int64_t ldx;
+    const void* gate;
+    int64_t ldg;
+    int64_t M;
+    int K;
+};
+
+// Threads a row has at most.
+template <typename T, int CH>
+constexpr int max_row_threads() { return kHeldCols / (kVec<T> * CH) < 1024 ? kHeldCols / (kVec<T> * CH) : 1024; }
+
+template <typename T, int CH, bool SHIFT, bool GATE>
+__global__ void __launch_bounds__(max_row_threads<T, CH>()) quantize_tokens_kernel(const TokenArgs a, int warps)
+{
+    constexpr int VEC = kVec<T>;
+    __shared__ uint32_t part_top[32];
+    __shared__ int part_sum[32];
+    const int tid = threadIdx.x % (32 * warps), row = threadIdx.x / (32 * warps), warp = tid >> 5;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (32 * warps)) + row;
+    const bool live = m < a.M;
+    const T* x = static_cast<const T*>(a.X) + m * a.ldx;
+    const T* gate = static_cast<const T*>(a.gate) + m * a.ldg;
+    T* hat = static_cast<T*>(a.hat) + m * a.ldh;
+    const int k0 = tid * VEC - (SHIFT ? lead_of<T>(a.hat ? hat : x) : 0);
+    uint4 xr[CH], gr[GATE ? CH : 1];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        xr[i] = load_chunk<T, SHIFT>(x, k0 + i * 32 * warps * VEC, a.K, live);
+        if (GATE) gr[i] = load_chunk<T, SHIFT>(gate, k0 + i * 32 * warps * VEC, a.K, live);
+    }
+    // what is kept through the reduction: 16-bit values as they are, else float32
+    constexpr bool PACKED = !GATE && sizeof(T) == 2;
+    float v[PACKED ? 1 : CH][VEC];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        if constexpr (PACKED) {   // two magnitudes at a time
+            const uint32_t mask = 0x7fff7fffu;
+            top = __vmaxu2(__vmaxu2(top, xr[i].x & mask),
+                           __vmaxu2(xr[i].y & mask, __vmaxu2(xr[i].z & mask, xr[i].w & mask)));
+        } else {
+            widen_chunk<T>(xr[i], v[i]);
+            if (GATE) {
+                float s[VEC];
+                widen_chunk<T>(gr[i], s);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[i][j] *= silu(s[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) top = max(top, magnitude(v[i][j]));
+        }
+    }
+    if constexpr (PACKED) {
+        float two[2];
+        widen(top, x, two);
+        top = max(__float_as_uint(two[0]), __float_as_uint(two[1]));
+    }
+    constexpr bool ELEVEN = PACKED && std::is_same<T, __half>::value;
+    const TokenGrid g = token_grid<ELEVEN>(row_max(top, part_top, row, warps, warp));
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int k = k0 + i * 32 * warps * VEC;
+        float(&w)[VEC] = v[PACKED ? 0 : i];
+        if constexpr (PACKED) widen_chunk<T>(xr[i], w);
+        code_chunk<VEC, ELEVEN, !GATE && sizeof(T) == 4>(w, g);
+        sum += store_codes<VEC, SHIFT>(a.Xq ? a.Xq + m * a.ldq : nullptr, k, a.K, live, w);
+        if (a.hat && live && k < a.K) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w[j] = (w[j] - kRound) * g.scale;
+            store_chunk<T, SHIFT>(hat, k, a.K, w);
+        }
+    }
+    if (a.x_sums) {
+        sum = row_sum_first(sum, part_sum, row, warps, warp);
+        if (live && tid == 0) a.x_sums[m] = sum;
+    }
+    if (live && tid == 0) a.x_scales[m] = g.scale;
+}
+
+template <typename T, int CH, bool SHIFT, bool GATE>
+__global__ void __launch_bounds__(max_row_threads<T, CH>()) block_norm_kernel(const BlockNormArgs a, int warps)
+{
+    constexpr int VEC = kVec<T>;
+    __shared__ float part_post[32], part_pre[32];
+    __shared__ uint32_t part_top[32];
+    __shared__ int part_sum[32];
+    const int tid = threadIdx.x % (32 * warps), row = threadIdx.x / (32 * warps), warp = tid >> 5;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (32 * warps)) + row;
+    const bool live = m < a.M;
+    const int D = static_cast<int>(a.D);
+    const T* block = static_cast<const T*>(a.block) + m * a.ldb;
+    const T* residual = static_cast<const T*>(a.residual) + m * a.ldr;
+    const T* gate = static_cast<const T*>(a.gate) + (GATE && live ? m / a.gate_rows : 0) * a.ldg;
+    T* stream_out = static_cast<T*>(a.stream_out) + m * a.lds;
+    T* out = static_cast<T*>(a.out) + m * a.ldo;
+    const int k0 = tid * VEC - (SHIFT ? lead_of<T>(a.stream_out ? stream_out : a.out ? out : a.block ? block : residual) : 0);
+    const int step = 32 * warps * VEC;
+    uint4 br[CH], rr[CH], gr[GATE ? CH : 1];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        br[i] = load_chunk<T, SHIFT>(block, k0 + i * step, D, live && a.block);
+        rr[i] = load_chunk<T, SHIFT>(residual, k0 + i * step, D, live && a.residual);
+        if (GATE) gr[i] = load_chunk<T, SHIFT>(gate, k0 + i * step, D, live);
+    }
+    float h[CH][VEC];
+    float scale = a.scale, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int k = k0 + i * step;
+        widen_chunk<T>(br[i], h[i]);
+        if (a.post_norm) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s = fmaf(h[i][j], h[i][j], s);
+            if (a.post_weight && k < D) times_weights<VEC, SHIFT>(h[i], a.post_weight, k, D);
+        }
+        if (GATE) {
+            float f[VEC];
+            widen_chunk<T>(gr[i], f);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) h[i][j] *= f[j];
+        }
+    }
+    if (a.block && a.post_norm)
+        scale *= rsqrtf(row_sum(s, part_post, row, warps, warp) / static_cast<float>(D) + a.eps);
+    s = 0.f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int k = k0 + i * step;
+        float r[VEC];
+        widen_chunk<T>(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            h[i][j] = a.block ? fmaf(scale, h[i][j], r[j]) : r[j];
+            s = fmaf(h[i][j], h[i][j], s);
+        }
+        if (live && k < D) {
+            if (a.stream_out) store_chunk<T, SHIFT>(stream_out, k, D, h[i]);
+            if (a.pre_weight) times_weights<VEC, SHIFT>(h[i], a.pre_weight, k, D);
+        }
+        if (a.q) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) top = max(top, magnitude(h[i][j]));
+        }
+    }
+    if (!a.out && !a.q) return;
+    const float pre = rsqrtf(row_sum(s, part_pre, row, warps, warp) / static_cast<float>(D) + a.eps);
+    if (a.out) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int k = k0 + i * step;
+            float f[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[j] = h[i][j] * pre;
+            if (live && k < D) store_chunk<T, SHIFT>(out, k, D, f);
+        }
+    }
+    if (!a.q) return;
+    // the codes are those of r' w: the factor rsqrt(...) of the row cancels in 127 v / t
+    const TokenGrid g = token_grid<false>(row_max(top, part_top, row, warps, warp));
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        code_chunk<VEC, false, false>(h[i], g);
+        sum += store_codes<VEC, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i]);
+    }
+    if (a.q_sums) {
+        sum = row_sum_first(sum, part_sum, row, warps, warp);
+        if (live && tid == 0) a.q_sums[m] = sum;
+    }
+    if (live && tid == 0) a.q_scales[m] = g.scale * pre;
+}
+
+// -- rows longer than kHeldCols: one block a row, which reads it again (from
+// L2) for each pass over it, element by element
+
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) quantize_wide_tokens_kernel(const TokenArgs a)
+{
+    __shared__ uint32_t part_top[32];
+    __shared__ int part_sum[32];
     const int64_t m = blockIdx.x;
+    const int warps = kWideThreads / 32, warp = threadIdx.x >> 5;
+    const T* x = static_cast<const T*>(a.X) + m * a.ldx;
+    const T* gate = a.gate ? static_cast<const T*>(a.gate) + m * a.ldg : nullptr;
     auto value = [&](int k) {
-        const float x = load_as_f32(X + m * ldx + k);
-        return gate ? silu(load_as_f32(gate + m * ldg + k)) * x : x;
+        const float v = load_as_f32(x + k);
+        return gate ? v * silu(load_as_f32(gate + k)) : v;
     };
     uint32_t top = 0;
-    for (int k = threadIdx.x; k < K; k += kRowThreads)
-        top = max(top, __float_as_uint(value(k)) & 0x7fffffffu);
-    const TokenGrid g = token_grid(block_reduce(top, Max()));
+    for (int k = threadIdx.x; k < a.K; k += kWideThreads) top = max(top, magnitude(value(k)));
+    top = row_max(top, part_top, 0, warps, warp);
+    const TokenGrid g = gate ? token_grid<false>(top) : token_grid<std::is_same<T, __half>::value>(top);
     int sum = 0;
-    for (int k = threadIdx.x; k < K; k += kRowThreads) {
-        const int q = !g.ok ? 0 : gate ? token_code<false>(value(k), g) : token_code<sizeof(T) == 4>(value(k), g);
-        sum += q;
-        if (Xq) Xq[m * ldq + k] = static_cast<int8_t>(q);
-        if (hat) store_rounded(hat + m * ldh + k, g.scale * static_cast<float>(q));
+    for (int k = threadIdx.x; k < a.K; k += kWideThreads) {
+        float v[1] = {value(k)};
+        if (gate)
+            code_chunk<1, false, false>(v, g);
+        else
+            code_chunk<1, std::is_same<T, __half>::value, sizeof(T) == 4>(v, g);
+        const float q = v[0] - kRound;
+        sum += static_cast<int>(q);
+        if (a.Xq) a.Xq[m * a.ldq + k] = static_cast<int8_t>(q);
+        if (a.hat) store_rounded(static_cast<T*>(a.hat) + m * a.ldh + k, q * g.scale);
     }
-    if (x_sums) {
-        sum = block_reduce(sum, Add());
-        if (threadIdx.x == 0) x_sums[m] = sum;
+    if (a.x_sums) {
+        sum = row_sum_first(sum, part_sum, 0, warps, warp);
+        if (threadIdx.x == 0) a.x_sums[m] = sum;
     }
-    if (x_scales && threadIdx.x == 0) x_scales[m] = g.scale;
+    if (threadIdx.x == 0) a.x_scales[m] = g.scale;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
-    block_norm_kernel(BlockNormArgs a)
+__global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const BlockNormArgs a)
 {
+    __shared__ float part_post[32], part_pre[32];
+    __shared__ uint32_t part_top[32];
+    __shared__ int part_sum[32];
     const int64_t m = blockIdx.x;
+    const int warps = kWideThreads / 32, warp = threadIdx.x >> 5;
     const int D = static_cast<int>(a.D);
-    const T* block = static_cast<const T*>(a.block);
-    const T* residual = static_cast<const T*>(a.residual);
-    const T* gate = static_cast<const T*>(a.gate);
-    float post = 1.f;
+    const T* block = a.block ? static_cast<const T*>(a.block) + m * a.ldb : nullptr;
+    const T* residual = a.residual ? static_cast<const T*>(a.residual) + m * a.ldr : nullptr;
+    const T* gate = a.gate ? static_cast<const T*>(a.gate) + (m / a.gate_rows) * a.ldg : nullptr;
+    float scale = a.scale;
     if (block && a.post_norm) {
         float s = 0.f;
-        for (int k = threadIdx.x; k < D; k += kRowThreads) {
-            const float h = load_as_f32(block + m * a.ldb + k);
+        for (int k = threadIdx.x; k < D; k += kWideThreads) {
+            const float h = load_as_f32(block + k);
             s = fmaf(h, h, s);
         }
-        post = rsqrtf(block_reduce(s, Add()) / static_cast<float>(D) + a.eps);
+        scale *= rsqrtf(row_sum(s, part_post, 0, warps, warp) / static_cast<float>(D) + a.eps);
     }
-    const int64_t grow = gate ? (m / a.gate_rows) * a.ldg : 0;
     auto value = [&](int k) {
-        float r = residual ? load_as_f32(residual + m * a.ldr + k) : 0.f;
+        const float r = residual ? load_as_f32(residual + k) : 0.f;
         if (!block) return r;
-        float h = load_as_f32(block + m * a.ldb + k) * post;
+        float h = load_as_f32(block + k);
         if (a.post_norm && a.post_weight) h *= a.post_weight[k];
-        if (gate) h *= load_as_f32(gate + grow + k);
-        return fmaf(a.scale, h, r);
+        if (gate) h *= load_as_f32(gate + k);
+        return fmaf(scale, h, r);
     };
+    auto weighted = [&](float r, int k) { return a.pre_weight ? r * a.pre_weight[k] : r; };
     float s = 0.f;
     uint32_t top = 0;
-    for (int k = threadIdx.x; k < D; k += kRowThreads) {
+    for (int k = threadIdx.x; k < D; k += kWideThreads) {
         const float r = value(k);
         s = fmaf(r, r, s);
-        top = max(top, __float_as_uint(a.pre_weight ? r * a.pre_weight[k] : r) & 0x7fffffffu);
+        top = max(top, magnitude(weighted(r, k)));
     }
-    const float pre = rsqrtf(block_reduce(s, Add()) / static_cast<float>(D) + a.eps);
-    // the codes are those of r w: the factor rsqrt(...) of the row cancels in 127 v / t
-    TokenGrid g = token_grid(block_reduce(top, Max()));
+    const float pre = rsqrtf(row_sum(s, part_pre, 0, warps, warp) / static_cast<float>(D) + a.eps);
+    const TokenGrid g = token_grid<false>(row_max(top, part_top, 0, warps, warp));
     int sum = 0;
-    for (int k = threadIdx.x; k < D; k += kRowThreads) {
+    for (int k = threadIdx.x; k < D; k += kWideThreads) {
         const float r = value(k);
-        const float v = a.pre_weight ? r * a.pre_weight[k] : r;
-        if (a.out) store_rounded(static_cast<T*>(a.out) + m * a.ldo + k, v * pre);
+        float v[1] = {weighted(r, k)};
+        if (a.out) store_rounded(static_cast<T*>(a.out) + m * a.ldo + k, v[0] * pre);
+        if (a.stream_out) store_rounded(static_cast<T*>(a.stream_out) + m * a.lds + k, r);
         if (a.q) {
-            const int q = g.ok ? token_code<false>(v, g) : 0;
-            sum += q;
+            code_chunk<1, false, false>(v, g);
+            const float q = v[0] - kRound;
+            sum += static_cast<int>(q);
             a.q[m * a.ldq + k] = static_cast<int8_t>(q);
         }
-        if (a.stream_out) store_rounded(static_cast<T*>(a.stream_out) + m * a.lds + k, r);
     }
-    if (a.q && a.q_sums) {
-        sum = block_reduce(sum, Add());
+    if (!a.q) return;
+    if (a.q_sums) {
+        sum = row_sum_first(sum, part_sum, 0, warps, warp);
         if (threadIdx.x == 0) a.q_sums[m] = sum;
     }
-    if (a.q && threadIdx.x == 0) a.q_scales[m] = g.scale * pre;
+    if (threadIdx.x == 0) a.q_scales[m] = g.scale * pre;
 }
 
 __global__ void w8a8_pack_kernel(int8_t* Wq, int64_t ldw, int32_t* w_zeros, const uint8_t* codes,
@@ -193,41 +669,105 @@ __global__ void w8a8_pack_kernel(int8_t* Wq, int64_t ldw, int32_t* w_zeros, cons
     if (blockIdx.x == 0 && threadIdx.x == 0) w_zeros[n] = static_cast<int32_t>(zeros[n]) - 128;
 }
 
+// ------------------------------------------------------------------- host
+// Rows of whole, aligned 16-byte chunks (what is absent passes).
+template <typename T>
+bool chunks_ok(const void* p, int64_t ld)
+{
+    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(T) % 16 == 0);
+}
+
+// Launches kernel(args, warps of a row): `cols` elements a row with what a
+// row off its boundaries needs in front, CH chunks a thread, at least four
+// warps a block.
+template <typename T, int CH, typename Args>
+int launch_rows(void (*kernel)(Args, int), const Args& args, int64_t M, int64_t cols, cudaStream_t stream)
+{
+    const int warps = static_cast<int>((cols + 32 * kVec<T> * CH - 1) / (32 * kVec<T> * CH));
+    const int rows = std::max(1, 4 / warps);
+    kernel<<<static_cast<unsigned>((M + rows - 1) / rows), 32 * warps * rows, 0, stream>>>(args, warps);
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+}
+
+// Chunks a thread: one where there are few rows (the latency of a row counts)
+// or a row is one warp's anyway, else up to four, which keep more bytes on
+// their way a thread and need fewer warps to meet.
+template <typename T>
+int chunks_a_thread(int64_t M, int64_t cols)
+{
+    const int64_t chunks = (cols + kVec<T> - 1) / kVec<T>;
+    if (M <= 2 * sm_count() && chunks <= 1024) return 1;
+    return chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
+}
+
+template <typename T, bool SHIFT, bool GATE>
+int tokens_chunked(const TokenArgs& a, cudaStream_t stream)
+{
+    const int64_t cols = a.K + (SHIFT ? kVec<T> - 1 : 0);
+    switch (chunks_a_thread<T>(a.M, cols)) {
+        case 1: return launch_rows<T, 1>(quantize_tokens_kernel<T, 1, SHIFT, GATE>, a, a.M, cols, stream);
+        case 2: return launch_rows<T, 2>(quantize_tokens_kernel<T, 2, SHIFT, GATE>, a, a.M, cols, stream);
+        default: return launch_rows<T, 4>(quantize_tokens_kernel<T, 4, SHIFT, GATE>, a, a.M, cols, stream);
+    }
+}
+
+template <typename T>
+int tokens_typed(const TokenArgs& a, cudaStream_t stream)
+{
+    const bool whole = a.K % kVec<T> == 0 && chunks_ok<T>(a.X, a.ldx) && chunks_ok<T>(a.gate, a.ldg) && chunks_ok<T>(a.hat, a.ldh);
+    if (a.K + (whole ? 0 : kVec<T> - 1) > kHeldCols) {
+        quantize_wide_tokens_kernel<T><<<static_cast<unsigned>(a.M), kWideThreads, 0, stream>>>(a);
+        GPTQ_LAUNCH_CHECK();
+        return GPTQ_OK;
+    }
+    if (whole) return a.gate ? tokens_chunked<T, false, true>(a, stream) : tokens_chunked<T, false, false>(a, stream);
+    return a.gate ? tokens_chunked<T, true, true>(a, stream) : tokens_chunked<T, true, false>(a, stream);
+}
+
+template <typename T, bool SHIFT, bool GATE>
+int norm_chunked(const BlockNormArgs& a, cudaStream_t stream)
+{
+    const int64_t cols = a.D + (SHIFT ? kVec<T> - 1 : 0);
+    switch (chunks_a_thread<T>(a.M, cols)) {
+        case 1: return launch_rows<T, 1>(block_norm_kernel<T, 1, SHIFT, GATE>, a, a.M, cols, stream);
+        case 2: return launch_rows<T, 2>(block_norm_kernel<T, 2, SHIFT, GATE>, a, a.M, cols, stream);
+        default: return launch_rows<T, 4>(block_norm_kernel<T, 4, SHIFT, GATE>, a, a.M, cols, stream);
+    }
+}
+
+template <typename T>
+int norm_typed(const BlockNormArgs& a, cudaStream_t stream)
+{
+    const bool whole = a.D % kVec<T> == 0 && chunks_ok<T>(a.block, a.ldb) && chunks_ok<T>(a.residual, a.ldr) &&
+                       chunks_ok<T>(a.gate, a.ldg) && chunks_ok<T>(a.out, a.ldo) && chunks_ok<T>(a.stream_out, a.lds) &&
+                       chunks_ok<float>(a.post_weight, 4) && chunks_ok<float>(a.pre_weight, 4);
+    if (a.D + (whole ? 0 : kVec<T> - 1) > kHeldCols) {
+        block_norm_wide_kernel<T><<<static_cast<unsigned>(a.M), kWideThreads, 0, stream>>>(a);
+        GPTQ_LAUNCH_CHECK();
+        return GPTQ_OK;
+    }
+    if (whole) return a.gate ? norm_chunked<T, false, true>(a, stream) : norm_chunked<T, false, false>(a, stream);
+    return a.gate ? norm_chunked<T, true, true>(a, stream) : norm_chunked<T, true, false>(a, stream);
+}
+
 }  // namespace
 
 int run_quantize_tokens(int8_t* Xq, int64_t ldq, float* x_scales, int32_t* x_sums, void* hat,
                         int64_t ldh, const void* X, int64_t ldx, const void* gate, int64_t ldg,
                         int type, int64_t M, int64_t K, cudaStream_t stream)
 {
-    const unsigned blocks = static_cast<unsigned>(M);
-    const int k = static_cast<int>(K);
-    if (type == GPTQ_F32)
-        quantize_tokens_kernel<<<blocks, kRowThreads, 0, stream>>>(
-            Xq, ldq, x_scales, x_sums, static_cast<float*>(hat), ldh, static_cast<const float*>(X),
-            ldx, static_cast<const float*>(gate), ldg, k);
-    else if (type == GPTQ_F16)
-        quantize_tokens_kernel<<<blocks, kRowThreads, 0, stream>>>(
-            Xq, ldq, x_scales, x_sums, static_cast<__half*>(hat), ldh, static_cast<const __half*>(X),
-            ldx, static_cast<const __half*>(gate), ldg, k);
-    else
-        quantize_tokens_kernel<<<blocks, kRowThreads, 0, stream>>>(
-            Xq, ldq, x_scales, x_sums, static_cast<__nv_bfloat16*>(hat), ldh,
-            static_cast<const __nv_bfloat16*>(X), ldx, static_cast<const __nv_bfloat16*>(gate), ldg, k);
-    GPTQ_LAUNCH_CHECK();
-    return GPTQ_OK;
+    const TokenArgs a{Xq, ldq, x_scales, x_sums, hat, ldh, X, ldx, gate, ldg, M, static_cast<int>(K)};
+    if (type == GPTQ_F32) return tokens_typed<float>(a, stream);
+    if (type == GPTQ_F16) return tokens_typed<__half>(a, stream);
+    return tokens_typed<__nv_bfloat16>(a, stream);
 }
 
 int run_block_norm(const BlockNormArgs& a, int type, cudaStream_t stream)
 {
-    const unsigned blocks = static_cast<unsigned>(a.M);
-    if (type == GPTQ_F32)
-        block_norm_kernel<float><<<blocks, kRowThreads, 0, stream>>>(a);
-    else if (type == GPTQ_F16)
-        block_norm_kernel<__half><<<blocks, kRowThreads, 0, stream>>>(a);
-    else
-        block_norm_kernel<__nv_bfloat16><<<blocks, kRowThreads, 0, stream>>>(a);
-    GPTQ_LAUNCH_CHECK();
-    return GPTQ_OK;
+    if (type == GPTQ_F32) return norm_typed<float>(a, stream);
+    if (type == GPTQ_F16) return norm_typed<__half>(a, stream);
+    return norm_typed<__nv_bfloat16>(a, stream);
 }
 
 int run_w8a8_pack(int8_t* Wq, int64_t ldw, int32_t* w_zeros, const uint8_t* codes, const float* zeros,

@@ -114,6 +114,18 @@ def test_tokens_ties_go_to_even(t):
         assert torch.equal(q.double(), torch.round(x.double() * 2 ** j))
 
 
+def test_tokens_ties_of_wide_maxima_float16():
+    """t = 127 s 2^-j with an odd s: the quotients of v = s (2 k + 1) 2^-(j + 1) are the ties k + 1/2."""
+    for s_ in (3, 5, 9, 11, 13, 15):
+        for j in (0, 4, 9):
+            k = torch.arange(-126, 126).double() + 0.5
+            v = torch.cat([torch.tensor([127.0]).double(), k, k.round()]) * s_ / 2 ** j
+            x = v[v.to(F16).double() == v][None].to(F16)
+            assert x[0, 0].double() == 127 * s_ / 2 ** j and x.numel() > 100
+            q, s, n, hat = _tokens(x)
+            assert torch.equal(q.double(), torch.round(_exact_codes(x.double())[0]))
+
+
 def test_tokens_next_to_ties_float32():
     """Values one and two steps of float32 from a tie."""
     top = torch.tensor([1.0, 3.0, 0.7, 1e-30, 3e38, 2.0 ** -149 * 12345], dtype=F32)
