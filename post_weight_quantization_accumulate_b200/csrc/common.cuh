@@ -99,6 +99,7 @@ struct BlockNormArgs {
     int post_norm;
     float scale, eps;
     int64_t M, D;
+    int64_t ahead;
 };
 struct W8A8Args {
     void* Y;

@@ -38,16 +38,13 @@ __device__ __forceinline__ void store_rounded(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_rounded(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_rounded(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ void widen(uint32_t w, const __half*, float* v)
+__device__ __forceinline__ float2 widen(uint32_t w, const __half*)
 {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    v[0] = f.x;
-    v[1] = f.y;
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-__device__ __forceinline__ void widen(uint32_t w, const __nv_bfloat16*, float* v)
+__device__ __forceinline__ float2 widen(uint32_t w, const __nv_bfloat16*)
 {
-    v[0] = __uint_as_float(w << 16);
-    v[1] = __uint_as_float(w & 0xffff0000u);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 __device__ __forceinline__ uint32_t narrow(float a, float b, const __half*)
 {
@@ -58,6 +55,35 @@ __device__ __forceinline__ uint32_t narrow(float a, float b, const __nv_bfloat16
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two neighbouring values at a time: one instruction for both.
+__device__ __forceinline__ uint64_t bits_of(float2 v)
+{
+    return static_cast<uint64_t>(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ float2 pair_of(uint64_t b)
+{
+    return make_float2(__uint_as_float(static_cast<uint32_t>(b)), __uint_as_float(static_cast<uint32_t>(b >> 32)));
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(c)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return pair_of(d);
 }
 
 // ---------------------------------------------------------------- chunks
@@ -104,6 +130,21 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Rows pass the L1 cache by, so that the weights stay in it.  (Not the
+// read-only path: a row may be written in place.)  Weights are float32.
+template <typename T, bool KEEP>
+__device__ __forceinline__ uint4 load16(const T* p)
+{
+    uint4 u;
+    if constexpr (KEEP)
+        u = __ldg(reinterpret_cast<const uint4*>(p));
+    else
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(p));
+    return u;
+}
+
 // The aligned 16 bytes at p, where one of them is between lo and hi: no byte
 // of another 16 is touched.
 __device__ __forceinline__ uint4 piece(uintptr_t p, uintptr_t lo, uintptr_t hi)
@@ -111,12 +152,12 @@ __device__ __forceinline__ uint4 piece(uintptr_t p, uintptr_t lo, uintptr_t hi)
     return p + 16 > lo && p < hi ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-template <typename T, bool SHIFT>
+template <typename T, bool SHIFT, bool KEEP = false>
 __device__ __forceinline__ uint4 load_chunk(const T* row, int k, int K, bool live)
 {
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (!SHIFT) {
-        return live && k < K ? *reinterpret_cast<const uint4*>(row + k) : zero;
+        return live && k < K ? load16<T, KEEP>(row + k) : zero;
     } else {
         if (!live || k >= K) return zero;
         const uintptr_t lo = reinterpret_cast<uintptr_t>(row), hi = lo + K * sizeof(T);
@@ -128,51 +169,56 @@ __device__ __forceinline__ uint4 load_chunk(const T* row, int k, int K, bool liv
     }
 }
 
+// A chunk in float32, as pairs.
 template <typename T>
-__device__ __forceinline__ void widen_chunk(uint4 u, float (&v)[kVec<T>])
+struct Chunk {
+    float2 v[kVec<T> / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Chunk<T> widen_chunk(uint4 u)
 {
+    Chunk<T> c;
     if constexpr (sizeof(T) == 4) {
-        v[0] = __uint_as_float(u.x);
-        v[1] = __uint_as_float(u.y);
-        v[2] = __uint_as_float(u.z);
-        v[3] = __uint_as_float(u.w);
+        c.v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        c.v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
     } else {
         const T* t = nullptr;
-        widen(u.x, t, v);
-        widen(u.y, t, v + 2);
-        widen(u.z, t, v + 4);
-        widen(u.w, t, v + 6);
+        c.v[0] = widen(u.x, t);
+        c.v[1] = widen(u.y, t);
+        c.v[2] = widen(u.z, t);
+        c.v[3] = widen(u.w, t);
     }
+    return c;
 }
 
 template <typename T, bool SHIFT>
-__device__ __forceinline__ void store_chunk(T* row, int k, int K, const float (&v)[kVec<T>])
+__device__ __forceinline__ void store_chunk(T* row, int k, int K, const Chunk<T>& c)
 {
     if (!SHIFT || (whole<T>(k, K) && reinterpret_cast<uintptr_t>(row + k) % 16 == 0)) {
         uint4 u;
         if constexpr (sizeof(T) == 4)
-            u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            u = make_uint4(__float_as_uint(c.v[0].x), __float_as_uint(c.v[0].y), __float_as_uint(c.v[1].x), __float_as_uint(c.v[1].y));
         else
-            u = make_uint4(narrow(v[0], v[1], row), narrow(v[2], v[3], row), narrow(v[4], v[5], row), narrow(v[6], v[7], row));
+            u = make_uint4(narrow(c.v[0].x, c.v[0].y, row), narrow(c.v[1].x, c.v[1].y, row), narrow(c.v[2].x, c.v[2].y, row),
+                           narrow(c.v[3].x, c.v[3].y, row));
         *reinterpret_cast<uint4*>(row + k) = u;
     } else {
 #pragma unroll
         for (int j = 0; j < kVec<T>; ++j)
-            if (k + j >= 0 && k + j < K) store_rounded(row + k + j, v[j]);
+            if (k + j >= 0 && k + j < K) store_rounded(row + k + j, j % 2 ? c.v[j / 2].y : c.v[j / 2].x);
     }
 }
 
-// v *= the float32 weights of the chunk's elements.
-template <int VEC, bool SHIFT>
-__device__ __forceinline__ void times_weights(float (&v)[VEC], const float* w, int k, int K)
+// c *= the float32 weights of the chunk's elements.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void times_weights(Chunk<T>& c, const float* w, int k, int K)
 {
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-        const uint4 u = load_chunk<float, SHIFT>(w, k + i, K, true);
-        v[i] *= __uint_as_float(u.x);
-        v[i + 1] *= __uint_as_float(u.y);
-        v[i + 2] *= __uint_as_float(u.z);
-        v[i + 3] *= __uint_as_float(u.w);
+    for (int i = 0; i < kVec<T> / 4; ++i) {
+        const Chunk<float> f = widen_chunk<float>(load_chunk<float, SHIFT, true>(w, k + 4 * i, K, true));
+        c.v[2 * i] = mul2(c.v[2 * i], f.v[0]);
+        c.v[2 * i + 1] = mul2(c.v[2 * i + 1], f.v[1]);
     }
 }
 
@@ -185,9 +231,28 @@ __device__ __forceinline__ int lead_of(const void* row)
 }
 
 // ------------------------------------------------------------- reductions
-// expf is good to 2 steps, the reciprocal and its product to 2 more; for a
-// far below 0 the reciprocal of an infinite sum is 0.
-__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.f + expf(-a)); }
+// silu(a) = a / (1 + exp(-a)).  Rounding -a log2(e) costs exp |a| half steps
+// of float32, the two approximations (2 steps and 1) and the rest 9.  Where
+// exp overflows the reciprocal is 0, and so is silu; an infinite negative a
+// gives NaN.
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 silu(float2 a)
+{
+    const float2 x = mul2(a, both(-1.44269504f));
+    const float2 d = add2(make_float2(exp2_approx(x.x), exp2_approx(x.y)), both(1.f));
+    return mul2(a, make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y)));
+}
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -197,15 +262,20 @@ __device__ __forceinline__ float warp_sum(float v)
 }
 
 // Over the `warps` warps of a row, the block's row-th.  Each reduction of a
-// kernel has slots of its own, so that one barrier each is enough.
+// kernel has slots of its own, so that one barrier each is enough.  A block
+// has several rows only where they have four warps at most.
+__device__ __forceinline__ int row_slot(int row, int warps) { return warps <= 4 ? 4 * row : 0; }
+
 __device__ __forceinline__ float row_sum(float v, float (&part)[32], int row, int warps, int warp)
 {
     v = warp_sum(v);
     if (warps == 1) return v;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) part[row * warps + warp] = v;
+    const float* p = part + row_slot(row, warps);
+    if (lane == 0) part[row_slot(row, warps) + warp] = v;
     __syncthreads();
-    return warp_sum(lane < warps ? part[row * warps + lane] : 0.f);
+    if (warps <= 4) return (p[0] + p[1]) + (warps > 2 ? p[2] + (warps > 3 ? p[3] : 0.f) : 0.f);
+    return warp_sum(lane < warps ? p[lane] : 0.f);
 }
 
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (&part)[32], int row, int warps, int warp)
@@ -213,9 +283,9 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (&part)[32], in
     v = __reduce_max_sync(0xffffffffu, v);
     if (warps == 1) return v;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) part[row * warps + warp] = v;
+    if (lane == 0) part[row_slot(row, warps) + warp] = v;
     __syncthreads();
-    return __reduce_max_sync(0xffffffffu, lane < warps ? part[row * warps + lane] : 0u);
+    return __reduce_max_sync(0xffffffffu, lane < warps ? part[row_slot(row, warps) + lane] : 0u);
 }
 
 // The sum ends up with the row's first warp.
@@ -224,9 +294,9 @@ __device__ __forceinline__ int row_sum_first(int v, int (&part)[32], int row, in
     v = __reduce_add_sync(0xffffffffu, v);
     if (warps == 1) return v;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) part[row * warps + warp] = v;
+    if (lane == 0) part[row_slot(row, warps) + warp] = v;
     __syncthreads();
-    return warp == 0 ? __reduce_add_sync(0xffffffffu, lane < warps ? part[row * warps + lane] : 0) : 0;
+    return warp == 0 ? __reduce_add_sync(0xffffffffu, lane < warps ? part[row_slot(row, warps) + lane] : 0) : 0;
 }
 
 // ------------------------------------------------------------------ codes
@@ -294,42 +364,49 @@ __device__ __forceinline__ float beside_tie(float v, float c, const TokenGrid& g
     return over ? c + side : c;
 }
 
-// v becomes kRound + its code.
-template <int VEC, bool ELEVEN, bool EXACT>
-__device__ __forceinline__ void code_chunk(float (&v)[VEC], const TokenGrid& g)
+// A pair becomes kRound + its codes.
+template <bool EXACT>
+__device__ __forceinline__ float2 multiplied(float2 v, const TokenGrid& g)
 {
-    if (g.kind == kZeros) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] = kRound;
-        return;
+    float2 c = fma2(v, both(g.r), both(kRound));
+    if (EXACT) {
+        const float2 f = fma2(v, both(g.r), make_float2(kRound - c.x, kRound - c.y));
+        if (fabsf(f.x) > 0.5f - 0x1p-13f) c.x = beside_tie(v.x, c.x, g);
+        if (fabsf(f.y) > 0.5f - 0x1p-13f) c.y = beside_tie(v.y, c.y, g);
     }
-    if (g.c != 1.f) {
+    return c;
+}
+
+template <bool ELEVEN, bool EXACT>
+__device__ __forceinline__ float2 code_pair(float2 v, const TokenGrid& g)
+{
+    if (g.kind == kZeros) return both(kRound);
+    if (g.c != 1.f) v = mul2(v, both(g.c));
+    if (!ELEVEN || g.kind == kMultiply) return multiplied<EXACT>(v, g);
+    const float rt = __frcp_rn(g.t);
+    auto code = [&](float x) {
+        const float a = 127.f * x, q = a * rt;
+        return kRound + fmaf(fmaf(-q, g.t, a), rt, q);
+    };
+    return make_float2(code(v.x), code(v.y));
+}
+
+template <typename T, bool ELEVEN, bool EXACT>
+__device__ __forceinline__ void code_chunk(Chunk<T>& c, const TokenGrid& g)
+{
+    if (g.kind == kMultiply && g.c == 1.f) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] *= g.c;
-    }
-    if (ELEVEN && g.kind == kDivide) {
-        const float rt = __frcp_rn(g.t);
+        for (int j = 0; j < kVec<T> / 2; ++j) c.v[j] = multiplied<EXACT>(c.v[j], g);
+    } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const float a = 127.f * v[j], q = a * rt;
-            v[j] = kRound + fmaf(fmaf(-q, g.t, a), rt, q);
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const float c = fmaf(v[j], g.r, kRound);
-        if (EXACT && fabsf(fmaf(v[j], g.r, kRound - c)) > 0.5f - 0x1p-13f)
-            v[j] = beside_tie(v[j], c, g);
-        else
-            v[j] = c;
+        for (int j = 0; j < kVec<T> / 2; ++j) c.v[j] = code_pair<ELEVEN, EXACT>(c.v[j], g);
     }
 }
 
-__device__ __forceinline__ uint32_t pack4(const float* v)
+__device__ __forceinline__ uint32_t pack4(float2 a, float2 b)
 {
-    return __byte_perm(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040),
-                       __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040), 0x5410);
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 
 // Stores the codes of the chunk at k (elements not there have code 0) and
@@ -337,14 +414,15 @@ __device__ __forceinline__ uint32_t pack4(const float* v)
 // chunks.  Off the boundaries of the codes' row a lane stores the word that
 // its chunk shares with the next lane's; at the warp's ends, and at the row's,
 // single codes.
-template <int VEC, bool SHIFT>
-__device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live, const float (&v)[VEC])
+template <typename T, bool SHIFT>
+__device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live, const Chunk<T>& c)
 {
+    constexpr int VEC = kVec<T>;
     uint32_t w[VEC / 4];
     int sum = 0;
 #pragma unroll
     for (int j = 0; j < VEC / 4; ++j) {
-        w[j] = pack4(v + 4 * j);
+        w[j] = pack4(c.v[2 * j], c.v[2 * j + 1]);
         sum = __dp4a(static_cast<int>(w[j]), 0x01010101, sum);
     }
     if (!row) return sum;
@@ -376,6 +454,17 @@ __device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live,
     return sum;
 }
 
+// Asks for row `m` of `cols` elements to be brought into L2 (its whole 16-byte
+// pieces).
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const T* rows, int64_t ld, int64_t m, int cols)
+{
+    const uintptr_t lo = (reinterpret_cast<uintptr_t>(rows + m * ld) + 15) & ~uintptr_t(15);
+    const uintptr_t hi = reinterpret_cast<uintptr_t>(rows + m * ld + cols) & ~uintptr_t(15);
+    if (hi > lo)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"(static_cast<uint32_t>(hi - lo)) : "memory");
+}
+
 // ---------------------------------------------------------------- kernels
 struct TokenArgs {
     int8_t* Xq;
@@ -390,14 +479,16 @@ struct TokenArgs {
     int64_t ldg;
     int64_t M;
     int K;
+    int64_t ahead;
 };
 
-// Threads a row has at most.
+// Threads a row has at most; with 1024 / that many blocks an SM at least, a
+// thread has 64 registers.
 template <typename T, int CH>
 constexpr int max_row_threads() { return kHeldCols / (kVec<T> * CH) < 1024 ? kHeldCols / (kVec<T> * CH) : 1024; }
 
 template <typename T, int CH, bool SHIFT, bool GATE>
-__global__ void __launch_bounds__(max_row_threads<T, CH>()) quantize_tokens_kernel(const TokenArgs a, int warps)
+__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) quantize_tokens_kernel(const TokenArgs a, int warps)
 {
     constexpr int VEC = kVec<T>;
     __shared__ uint32_t part_top[32];
@@ -409,6 +500,10 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>()) quantize_tokens_kern
     const T* gate = static_cast<const T*>(a.gate) + m * a.ldg;
     T* hat = static_cast<T*>(a.hat) + m * a.ldh;
     const int k0 = tid * VEC - (SHIFT ? lead_of<T>(a.hat ? hat : x) : 0);
+    if (tid == 0 && a.ahead && m + a.ahead < a.M) {
+        prefetch_row(static_cast<const T*>(a.X), a.ldx, m + a.ahead, a.K);
+        if (GATE) prefetch_row(static_cast<const T*>(a.gate), a.ldg, m + a.ahead, a.K);
+    }
     uint4 xr[CH], gr[GATE ? CH : 1];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -417,7 +512,7 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>()) quantize_tokens_kern
     }
     // what is kept through the reduction: 16-bit values as they are, else float32
     constexpr bool PACKED = !GATE && sizeof(T) == 2;
-    float v[PACKED ? 1 : CH][VEC];
+    Chunk<T> v[PACKED ? 1 : CH];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -426,21 +521,19 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>()) quantize_tokens_kern
             top = __vmaxu2(__vmaxu2(top, xr[i].x & mask),
                            __vmaxu2(xr[i].y & mask, __vmaxu2(xr[i].z & mask, xr[i].w & mask)));
         } else {
-            widen_chunk<T>(xr[i], v[i]);
+            v[i] = widen_chunk<T>(xr[i]);
             if (GATE) {
-                float s[VEC];
-                widen_chunk<T>(gr[i], s);
+                const Chunk<T> s = widen_chunk<T>(gr[i]);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) v[i][j] *= silu(s[j]);
+                for (int j = 0; j < VEC / 2; ++j) v[i].v[j] = mul2(v[i].v[j], silu(s.v[j]));
             }
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) top = max(top, magnitude(v[i][j]));
+            for (int j = 0; j < VEC / 2; ++j) top = max(max(top, magnitude(v[i].v[j].x)), magnitude(v[i].v[j].y));
         }
     }
     if constexpr (PACKED) {
-        float two[2];
-        widen(top, x, two);
-        top = max(__float_as_uint(two[0]), __float_as_uint(two[1]));
+        const float2 two = widen(top, x);
+        top = max(__float_as_uint(two.x), __float_as_uint(two.y));
     }
     constexpr bool ELEVEN = PACKED && std::is_same<T, __half>::value;
     const TokenGrid g = token_grid<ELEVEN>(row_max(top, part_top, row, warps, warp));
@@ -448,13 +541,13 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>()) quantize_tokens_kern
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int k = k0 + i * 32 * warps * VEC;
-        float(&w)[VEC] = v[PACKED ? 0 : i];
-        if constexpr (PACKED) widen_chunk<T>(xr[i], w);
-        code_chunk<VEC, ELEVEN, !GATE && sizeof(T) == 4>(w, g);
-        sum += store_codes<VEC, SHIFT>(a.Xq ? a.Xq + m * a.ldq : nullptr, k, a.K, live, w);
+        Chunk<T>& w = v[PACKED ? 0 : i];
+        if constexpr (PACKED) w = widen_chunk<T>(xr[i]);
+        code_chunk<T, ELEVEN, !GATE && sizeof(T) == 4>(w, g);
+        sum += store_codes<T, SHIFT>(a.Xq ? a.Xq + m * a.ldq : nullptr, k, a.K, live, w);
         if (a.hat && live && k < a.K) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) w[j] = (w[j] - kRound) * g.scale;
+            for (int j = 0; j < VEC / 2; ++j) w.v[j] = mul2(add2(w.v[j], both(-kRound)), both(g.scale));
             store_chunk<T, SHIFT>(hat, k, a.K, w);
         }
     }
@@ -466,7 +559,7 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>()) quantize_tokens_kern
 }
 
 template <typename T, int CH, bool SHIFT, bool GATE>
-__global__ void __launch_bounds__(max_row_threads<T, CH>()) block_norm_kernel(const BlockNormArgs a, int warps)
+__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) block_norm_kernel(const BlockNormArgs a, int warps)
 {
     constexpr int VEC = kVec<T>;
     __shared__ float part_post[32], part_pre[32];
@@ -483,63 +576,66 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>()) block_norm_kernel(co
     T* out = static_cast<T*>(a.out) + m * a.ldo;
     const int k0 = tid * VEC - (SHIFT ? lead_of<T>(a.stream_out ? stream_out : a.out ? out : a.block ? block : residual) : 0);
     const int step = 32 * warps * VEC;
+    if (tid == 0 && a.ahead && m + a.ahead < a.M) {
+        if (a.block) prefetch_row(static_cast<const T*>(a.block), a.ldb, m + a.ahead, D);
+        if (a.residual) prefetch_row(static_cast<const T*>(a.residual), a.ldr, m + a.ahead, D);
+        if (GATE && a.gate_rows == 1) prefetch_row(static_cast<const T*>(a.gate), a.ldg, m + a.ahead, D);
+    }
     uint4 br[CH], rr[CH], gr[GATE ? CH : 1];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         br[i] = load_chunk<T, SHIFT>(block, k0 + i * step, D, live && a.block);
         rr[i] = load_chunk<T, SHIFT>(residual, k0 + i * step, D, live && a.residual);
-        if (GATE) gr[i] = load_chunk<T, SHIFT>(gate, k0 + i * step, D, live);
+        if (GATE) gr[i] = load_chunk<T, SHIFT, true>(gate, k0 + i * step, D, live);
     }
-    float h[CH][VEC];
-    float scale = a.scale, s = 0.f;
+    float scale = a.block ? a.scale : 0.f;
+    if (a.block && a.post_norm) {
+        float2 s = both(0.f);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int k = k0 + i * step;
-        widen_chunk<T>(br[i], h[i]);
-        if (a.post_norm) {
+        for (int i = 0; i < CH; ++i) {
+            const Chunk<T> c = widen_chunk<T>(br[i]);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) s = fmaf(h[i][j], h[i][j], s);
-            if (a.post_weight && k < D) times_weights<VEC, SHIFT>(h[i], a.post_weight, k, D);
+            for (int j = 0; j < VEC / 2; ++j) s = fma2(c.v[j], c.v[j], s);
         }
-        if (GATE) {
-            float f[VEC];
-            widen_chunk<T>(gr[i], f);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) h[i][j] *= f[j];
-        }
+        scale *= rsqrtf(row_sum(s.x + s.y, part_post, row, warps, warp) / static_cast<float>(D) + a.eps);
     }
-    if (a.block && a.post_norm)
-        scale *= rsqrtf(row_sum(s, part_post, row, warps, warp) / static_cast<float>(D) + a.eps);
-    s = 0.f;
+    Chunk<T> h[CH];
+    float2 s = both(0.f);
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int k = k0 + i * step;
-        float r[VEC];
-        widen_chunk<T>(rr[i], r);
+        h[i] = widen_chunk<T>(br[i]);
+        if (a.post_norm && a.post_weight && k < D) times_weights<T, SHIFT>(h[i], a.post_weight, k, D);
+        if (GATE) {
+            const Chunk<T> f = widen_chunk<T>(gr[i]);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            h[i][j] = a.block ? fmaf(scale, h[i][j], r[j]) : r[j];
-            s = fmaf(h[i][j], h[i][j], s);
+            for (int j = 0; j < VEC / 2; ++j) h[i].v[j] = mul2(h[i].v[j], f.v[j]);
+        }
+        const Chunk<T> r = widen_chunk<T>(rr[i]);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            h[i].v[j] = fma2(both(scale), h[i].v[j], r.v[j]);
+            s = fma2(h[i].v[j], h[i].v[j], s);
         }
         if (live && k < D) {
             if (a.stream_out) store_chunk<T, SHIFT>(stream_out, k, D, h[i]);
-            if (a.pre_weight) times_weights<VEC, SHIFT>(h[i], a.pre_weight, k, D);
+            if (a.pre_weight) times_weights<T, SHIFT>(h[i], a.pre_weight, k, D);
         }
         if (a.q) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) top = max(top, magnitude(h[i][j]));
+            for (int j = 0; j < VEC / 2; ++j) top = max(max(top, magnitude(h[i].v[j].x)), magnitude(h[i].v[j].y));
         }
     }
     if (!a.out && !a.q) return;
-    const float pre = rsqrtf(row_sum(s, part_pre, row, warps, warp) / static_cast<float>(D) + a.eps);
+    const float pre = rsqrtf(row_sum(s.x + s.y, part_pre, row, warps, warp) / static_cast<float>(D) + a.eps);
     if (a.out) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int k = k0 + i * step;
-            float f[VEC];
+            Chunk<T> f;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) f[j] = h[i][j] * pre;
+            for (int j = 0; j < VEC / 2; ++j) f.v[j] = mul2(h[i].v[j], both(pre));
             if (live && k < D) store_chunk<T, SHIFT>(out, k, D, f);
         }
     }
@@ -549,8 +645,8 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>()) block_norm_kernel(co
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        code_chunk<VEC, false, false>(h[i], g);
-        sum += store_codes<VEC, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i]);
+        code_chunk<T, false, false>(h[i], g);
+        sum += store_codes<T, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i]);
     }
     if (a.q_sums) {
         sum = row_sum_first(sum, part_sum, row, warps, warp);
@@ -573,7 +669,7 @@ __global__ void __launch_bounds__(kWideThreads) quantize_wide_tokens_kernel(cons
     const T* gate = a.gate ? static_cast<const T*>(a.gate) + m * a.ldg : nullptr;
     auto value = [&](int k) {
         const float v = load_as_f32(x + k);
-        return gate ? v * silu(load_as_f32(gate + k)) : v;
+        return gate ? v * silu(both(load_as_f32(gate + k))).x : v;
     };
     uint32_t top = 0;
     for (int k = threadIdx.x; k < a.K; k += kWideThreads) top = max(top, magnitude(value(k)));
@@ -581,12 +677,9 @@ __global__ void __launch_bounds__(kWideThreads) quantize_wide_tokens_kernel(cons
     const TokenGrid g = gate ? token_grid<false>(top) : token_grid<std::is_same<T, __half>::value>(top);
     int sum = 0;
     for (int k = threadIdx.x; k < a.K; k += kWideThreads) {
-        float v[1] = {value(k)};
-        if (gate)
-            code_chunk<1, false, false>(v, g);
-        else
-            code_chunk<1, std::is_same<T, __half>::value, sizeof(T) == 4>(v, g);
-        const float q = v[0] - kRound;
+        const float2 v = both(value(k));
+        const float q =
+            (gate ? code_pair<false, false>(v, g) : code_pair<std::is_same<T, __half>::value, sizeof(T) == 4>(v, g)).x - kRound;
         sum += static_cast<int>(q);
         if (a.Xq) a.Xq[m * a.ldq + k] = static_cast<int8_t>(q);
         if (a.hat) store_rounded(static_cast<T*>(a.hat) + m * a.ldh + k, q * g.scale);
@@ -640,12 +733,11 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const Blo
     int sum = 0;
     for (int k = threadIdx.x; k < D; k += kWideThreads) {
         const float r = value(k);
-        float v[1] = {weighted(r, k)};
-        if (a.out) store_rounded(static_cast<T*>(a.out) + m * a.ldo + k, v[0] * pre);
+        const float v = weighted(r, k);
+        if (a.out) store_rounded(static_cast<T*>(a.out) + m * a.ldo + k, v * pre);
         if (a.stream_out) store_rounded(static_cast<T*>(a.stream_out) + m * a.lds + k, r);
         if (a.q) {
-            code_chunk<1, false, false>(v, g);
-            const float q = v[0] - kRound;
+            const float q = code_pair<false, false>(both(v), g).x - kRound;
             sum += static_cast<int>(q);
             a.q[m * a.ldq + k] = static_cast<int8_t>(q);
         }
@@ -757,14 +849,16 @@ int run_quantize_tokens(int8_t* Xq, int64_t ldq, float* x_scales, int32_t* x_sum
                         int64_t ldh, const void* X, int64_t ldx, const void* gate, int64_t ldg,
                         int type, int64_t M, int64_t K, cudaStream_t stream)
 {
-    const TokenArgs a{Xq, ldq, x_scales, x_sums, hat, ldh, X, ldx, gate, ldg, M, static_cast<int>(K)};
+    const TokenArgs a{Xq, ldq, x_scales, x_sums, hat, ldh, X, ldx, gate, ldg, M, static_cast<int>(K), 2 * sm_count()};
     if (type == GPTQ_F32) return tokens_typed<float>(a, stream);
     if (type == GPTQ_F16) return tokens_typed<__half>(a, stream);
     return tokens_typed<__nv_bfloat16>(a, stream);
 }
 
-int run_block_norm(const BlockNormArgs& a, int type, cudaStream_t stream)
+int run_block_norm(const BlockNormArgs& a0, int type, cudaStream_t stream)
 {
+    BlockNormArgs a = a0;
+    a.ahead = 2 * sm_count();
     if (type == GPTQ_F32) return norm_typed<float>(a, stream);
     if (type == GPTQ_F16) return norm_typed<__half>(a, stream);
     return norm_typed<__nv_bfloat16>(a, stream);
