@@ -327,21 +327,22 @@ def _rows(t, dtype, shape, name):
     """(address, row pitch) of a matrix whose rows are contiguous; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     # the pitch of a single row is not looked at: any that the library accepts
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else (shape[1] + 15) // 16 * 16
+    return t.data_ptr(), pitch if shape[0] > 1 else (shape[1] + 15) // 16 * 16
 
 
 def _vec(t, dtype, n, name):
     """Address of a contiguous vector of n elements; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
     if t.shape != (n,):
         raise ValueError(f"{name} must be [{n}]")
@@ -353,22 +354,34 @@ def _vec(t, dtype, n, name):
 def _type(t, name):
     if not isinstance(t, torch.Tensor) or t.dtype not in TYPES:
         raise TypeError(f"{name} must be a bfloat16, float16 or float32 tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
     return TYPES[t.dtype]
+
+
+# the stream's handle without a Stream object around it, where torch has that
+# (2 us of the 10 that a small call takes on the host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call_on(fn: str, t: torch.Tensor, others, stream, *args):
     """Calls `fn` with the device of `t` current, on `stream` or that device's
     current stream; every other tensor has to be on the same device."""
+    device = t.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
+        if o is not None and o.get_device() != device:
             raise ValueError("tensor arguments must be on one device")
-    f = getattr(lib(), fn)
-    if not t.is_cuda or t.device.index == torch.cuda.current_device():
-        st = f(*args, _stream(t, stream))
+    if device < 0:
+        raise ValueError("tensor arguments must be on a CUDA device")
+    f = getattr(_lib or lib(), fn)
+    s = _raw_stream(device) if stream is None and _raw_stream else _stream(t, stream)
+    if device == torch.cuda.current_device():
+        st = f(*args, s)
     else:
-        with torch.cuda.device(t.device):
-            st = f(*args, _stream(t, stream))
-    _check(fn, st)
+        with torch.cuda.device(device):
+            st = f(*args, s)
+    if st != GPTQ_OK:
+        raise GptqError(fn, st)
 
 
 def gptq_quantize_tokens(Xq: torch.Tensor | None, x_scales: torch.Tensor, x_sums: torch.Tensor | None,

@@ -32,7 +32,8 @@ class Weight:
 
 def empty_codes(rows: int, cols: int, device) -> torch.Tensor:
     """int8 [rows, cols] at the pitch the 8-bit calls take."""
-    return torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8, device=device)[:, :cols]
+    codes = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8, device=device)
+    return codes if cols % 16 == 0 else codes[:, :cols]
 
 
 def pack(layer) -> Weight:
