@@ -23,9 +23,12 @@ __device__ __forceinline__ uint32_t cta_rank()
     return r;
 }
 
+__device__ __forceinline__ void arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    arrive();
+    wait();
 }
 
 __device__ __forceinline__ void arrive_on(uint32_t bar)

@@ -17,22 +17,30 @@
 //
 //  * pair kernel: 256 weight rows x NT tokens by a pair of CTAs (cta_group::2),
 //    persistent, double-buffered accumulators, so that the scaling and the
-//    stores of a tile overlap the products of the next.
+//    stores of a tile overlap the products of the next.  Bound by the tensor
+//    cores and, at full load, by the card's power: 8192 x 4096 x 11008 232 us
+//    back to back (3180 TOP/s), 205 us alone (3600).
 //  * split kernel: 128 weight rows x NT tokens by a cluster of CTAs that share
 //    K and add their partial sums through distributed shared memory: for few
 //    tokens, where the weights' way from memory is what counts and one tile a
-//    CTA would leave SMs without work.
-//  * few kernel (up to 16 tokens): 16 weight rows a block, the warps take turns
-//    along K and feed mma.sync straight from global loads.  Nothing but the
-//    weights' bytes counts there, and the set-up of tensor memory, barriers and
-//    clusters costs more than the products: 1 x 4096 x 4096 3.6 us against 7.9
-//    by the split kernel, 16 x 4096 x 11008 12.4 against 14.6, 32 x 4096 x
-//    11008 22.7 against 15.0 (the tokens' rows are read again by each block).
+//    CTA would leave SMs without work.  24 x 11008 x 4096 11.9 us (3.8 TB/s; 7
+//    of them the weights' bytes, 3.8 a call of one stage).
+//  * few kernel (8 tokens, or a few more of small weights): 16 weight rows a
+//    block, the warps take turns along K and feed mma.sync straight from
+//    global loads.  Nothing but the weights' bytes counts there, and the set-up
+//    of tensor memory, barriers and clusters costs more than the products.
+//    1 x 4096 x 4096 3.6 us (4.7 TB/s), 1 x 28672 x 8192 38.5 us (6.1 TB/s).
+//
+// The two threads of a CTA that issue loads and MMAs are the elected ones of
+// their warps: under a plain lane test every such instruction took about 110
+// cycles to issue instead of 45, and with that the issue bound the kernels
+// (24 x 4096 x 4096 8.2 us against 6.1, 8192 x 11008 x 4096 270 against 245).
 #include "pair.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <mutex>
 
 namespace gptq {
@@ -47,6 +55,37 @@ constexpr int kWBytes = kRows * kBK;
 __device__ __forceinline__ void store_rounded(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_rounded(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_rounded(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// The first `left` (at most 4) of four neighbouring outputs.
+__device__ __forceinline__ void store4(float* p, int64_t left, float a, float b, float c, float d)
+{
+    if (left >= 4 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+        *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+        return;
+    }
+    if (left > 0) p[0] = a;
+    if (left > 1) p[1] = b;
+    if (left > 2) p[2] = c;
+    if (left > 3) p[3] = d;
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, int64_t left, float a, float b, float c, float d)
+{
+    T v[4];
+    store_rounded(v, a);
+    store_rounded(v + 1, b);
+    store_rounded(v + 2, c);
+    store_rounded(v + 3, d);
+    if (left >= 4 && reinterpret_cast<uintptr_t>(p) % 8 == 0) {
+        uint2 u;
+        memcpy(&u, v, 8);
+        *reinterpret_cast<uint2*>(p) = u;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < left) p[j] = v[j];
+}
 
 // Instruction descriptor of kind::i8: 32-bit integer sums of signed 8-bit
 // operands, both K-major.
@@ -74,16 +113,47 @@ __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_
             : "memory");
 }
 
-// The MMAs of one stage: `codes` codes of K from the rows at w and x.
+// The MMAs of one stage: `codes` codes of K (or all of them) from the
+// descriptors of its two operands.
 template <int GROUP>
-__device__ __forceinline__ void stage_mmas(uint32_t d, const uint8_t* w, const uint8_t* x, uint32_t idesc, int codes, bool first)
+__device__ __forceinline__ void stage_mmas(uint32_t d, uint64_t wd, uint64_t xd, uint32_t idesc, int codes, bool first)
 {
-    const uint64_t wd = sdesc_sw128(smem_u32(w), 16, 1024);
-    const uint64_t xd = sdesc_sw128(smem_u32(x), 16, 1024);
+    umma_i8<GROUP>(d, wd, xd, idesc, first ? 0u : 1u);
+    if (codes >= kBK) {
 #pragma unroll
-    for (int k = 0; k < kBK / kStep; ++k)
-        if (k * kStep < codes)
-            umma_i8<GROUP>(d, wd + k * (kStep >> 4), xd + k * (kStep >> 4), idesc, first && k == 0 ? 0u : 1u);
+        for (int k = 1; k < kBK / kStep; ++k) umma_i8<GROUP>(d, wd + k * (kStep >> 4), xd + k * (kStep >> 4), idesc, 1u);
+    } else {
+        for (int k = 1; k * kStep < codes; ++k) umma_i8<GROUP>(d, wd + k * (kStep >> 4), xd + k * (kStep >> 4), idesc, 1u);
+    }
+}
+
+// True for one lane of a converged warp.  The compiler knows that one thread
+// runs what it guards and issues tcgen05 instructions there straight.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(one));
+    return one != 0;
+}
+
+// The accumulators of a lane, 16 or 32 columns.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, int (&v)[16])
+{
+    float f[16];
+    tmem_ld_32x32b_x16(taddr, f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __float_as_int(f[i]);
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, int (&v)[32])
+{
+    float f[32];
+    tmem_ld_32x32b_x32(taddr, f);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_int(f[i]);
 }
 
 // What the outputs of one weight row n share.
@@ -117,8 +187,11 @@ __device__ __forceinline__ float output(int acc, const RowScale& r, uint2 t)
 }
 
 // ------------------------------------------------------------- pair kernel
-constexpr int kPairThreads = 384;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
+constexpr int kPairThreads = 128 + 32 * kEpiWarps;
+// Between its looks at a barrier a waiting epilogue warp sleeps this long (ns):
+// sixteen polling warps slow the two threads that issue the loads and MMAs.
+constexpr unsigned kNap = 100;
 
 template <int NT>
 struct alignas(1024) PairSmem {
@@ -191,8 +264,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     volatile int* abort = &S.abort;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
+        if (elect_one()) {
+            uint32_t it = 0, phase = 1;
+            int s = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += n_pairs) {
                 int tn, tm;
@@ -200,12 +274,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const int n0 = tn * 2 * kRows + static_cast<int>(rank) * kRows;
                 const int m0 = tm * NT + static_cast<int>(rank) * (NT / 2);
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait_bounded(&S.empty[s], ((it / kStages) & 1) ^ 1, abort, status)) { ok = false; break; }
+                    if (!mbar_wait_bounded(&S.empty[s], phase, abort, status)) { ok = false; break; }
                     if (rank == 0) mbar_arrive_expect_tx(&S.full[s], 2 * Smem::kStageBytes);
                     const uint32_t bar = cluster::map_address(&S.full[s], 0);
                     cluster::pair_tma_load_2d(S.stage[s], &mapW, bar, k * kBK, n0);
                     cluster::pair_tma_load_2d(S.stage[s] + kWBytes, &mapX, bar, k * kBK, m0);
+                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
             }
             // copies in flight land before the shared memory goes away: every
@@ -218,26 +292,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            uint32_t it = 0, i = 0;
+        if (rank == 0 && elect_one()) {
+            const uint64_t wd0 = sdesc_sw128(smem_u32(S.stage[0]), 16, 1024);
+            const uint64_t xd0 = sdesc_sw128(smem_u32(S.stage[0] + kWBytes), 16, 1024);
+            uint32_t i = 0, phase = 0;
+            int s = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += n_pairs, ++i) {
                 const int b = i & 1;
                 if (!mbar_wait_bounded(&S.tempty[b], ((i >> 1) & 1) ^ 1, abort, status)) break;
                 tc_fence_after();
-                for (int k = 0; k < nk; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait_bounded(&S.full[s], (it / kStages) & 1, abort, status)) { ok = false; break; }
+                for (int k = 0; k < nk; ++k) {
+                    if (!mbar_wait_bounded(&S.full[s], phase, abort, status)) { ok = false; break; }
                     tc_fence_after();
-                    stage_mmas<2>(tbase + b * NT, S.stage[s], S.stage[s] + kWBytes, idesc_i8(2 * kRows, NT), K - k * kBK, k == 0);
+                    stage_mmas<2>(tbase + b * NT, wd0 + s * (Smem::kStageBytes >> 4), xd0 + s * (Smem::kStageBytes >> 4),
+                                  idesc_i8(2 * kRows, NT), K - k * kBK, k == 0);
                     cluster::pair_commit(&S.empty[s]);
+                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
                 if (ok) cluster::pair_commit(&S.tfull[b]);
             }
         }
         __syncwarp();
     } else if (warp >= 4) {
-        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. +31, token half h
+        // epilogue: warp w reads TMEM lanes 32 (w % 4) .. +31, token quarter h
+        constexpr int kPart = 4 * NT / kEpiWarps;
+        constexpr int kCols = kPart < 32 ? kPart : 32;
         const int q = warp & 3;
         const int h = (warp - 4) >> 2;
         const int et = threadIdx.x - 128;
@@ -252,24 +332,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // the buffer's readers, two tiles ago, are past the last barrier
             if (et < NT) S.token[b][et] = token_scale(a, m0 + et);
             const RowScale r = row_scale(a, n);
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
             // after a wait that ran out every warp still takes part in the barriers of the tiles left
-            ok = ok && mbar_wait_warp(&S.tfull[b], (i >> 1) & 1, abort, status);
+            ok = ok && mbar_wait_warp(&S.tfull[b], (i >> 1) & 1, abort, status, kWaitLimitCycles, kNap);
             if (!ok) continue;
             tc_fence_after();
-            const uint32_t taddr = tbase + (static_cast<uint32_t>(q * 32) << 16) + b * NT + h * (NT / 2);
-            T* y = static_cast<T*>(a.Y) + (m0 + h * (NT / 2)) * a.ldy + n;
+            const uint32_t taddr = tbase + (static_cast<uint32_t>(q * 32) << 16) + b * NT + h * kPart;
+            T* y = static_cast<T*>(a.Y) + (m0 + h * kPart) * a.ldy + n;
 #pragma unroll 1
-            for (int c = 0; c < NT / 2; c += 32) {
-                float v[32];
-                tmem_ld_32x32b_x32(taddr + c, v);
+            for (int c = 0; c < kPart; c += kCols) {
+                int v[kCols];
+                tmem_ld_cols(taddr + c, v);
                 tmem_ld_wait();
-                const int64_t left = a.M - (m0 + h * (NT / 2) + c);
+                const int64_t left = a.M - (m0 + h * kPart + c);
                 if (n < a.N) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < kCols; ++j)
                         if (j < left) {
-                            store_rounded(y, output(__float_as_int(v[j]), r, S.token[b][h * (NT / 2) + c + j]));
+                            store_rounded(y, output(v[j], r, S.token[b][h * kPart + c + j]));
                             y += a.ldy;
                         }
                 }
@@ -296,6 +376,7 @@ constexpr int kMaxSplits = 8;
 
 struct SplitShared {
     uint64_t full[kMaxStages], empty[kMaxStages], done;
+    uint2 token[128];
     uint32_t tmem_base;
     int abort;
 };
@@ -320,7 +401,14 @@ __global__ void __launch_bounds__(kSplitThreads)
     const int k_begin = blocks * rank / splits, k_end = blocks * (rank + 1) / splits;
     const int nk = k_end - k_begin;
 
-    if (threadIdx.x == 0) {
+    auto load = [&](int k, int s) {
+        uint8_t* st = base + s * kStageBytes;
+        mbar_arrive_expect_tx(&S.full[s], kStageBytes);
+        tma_load_2d(st, &mapW, &S.full[s], (k_begin + k) * kBK, n0);
+        tma_load_2d(st + kWBytes, &mapX, &S.full[s], (k_begin + k) * kBK, m0);
+    };
+    const int first = min(stages, nk);
+    if (warp == 0 && elect_one()) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&S.full[s], 1);
             mbar_init(&S.empty[s], 1);
@@ -328,8 +416,8 @@ __global__ void __launch_bounds__(kSplitThreads)
         mbar_init(&S.done, 1);
         S.abort = 0;
         fence_mbar_init();
-        prefetch_tmap(&mapW);
-        prefetch_tmap(&mapX);
+        // the first loads are on their way before the block has met
+        for (int k = 0; k < first; ++k) load(k, k);
     }
     if (warp == 1) {
         tmem_alloc(&S.tmem_base, kCols);
@@ -341,16 +429,24 @@ __global__ void __launch_bounds__(kSplitThreads)
     const uint32_t tbase = S.tmem_base;
     volatile int* abort = &S.abort;
 
+    // This thread's outputs of the shared epilogue: four neighbouring weight
+    // rows, every sixth token of this CTA's part.  What they need is loaded
+    // before it is wanted.
+    const int64_t n = n0 + 4 * lane;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), a.M - m0));
+    const int t_end = tokens * (rank + 1) / splits;
+    RowScale rows[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rows[j] = row_scale(a, n + j);
+
     if (warp == 0) {
-        if (lane == 0) {
-            int k = 0;
+        if (elect_one()) {
+            int k = first, s = 0;
+            uint32_t phase = 0;
             for (; k < nk; ++k) {
-                const int s = k % stages;
-                if (!mbar_wait_bounded(&S.empty[s], ((k / stages) & 1) ^ 1, abort, status)) break;
-                uint8_t* st = base + s * kStageBytes;
-                mbar_arrive_expect_tx(&S.full[s], kStageBytes);
-                tma_load_2d(st, &mapW, &S.full[s], (k_begin + k) * kBK, n0);
-                tma_load_2d(st + kWBytes, &mapX, &S.full[s], (k_begin + k) * kBK, m0);
+                if (!mbar_wait_bounded(&S.empty[s], phase, abort, status)) break;
+                load(k, s);
+                if (++s == stages) { s = 0; phase ^= 1; }
             }
             // after a wait that ran out: the copies issued land before the shared memory goes away
             int none = 0;
@@ -360,70 +456,82 @@ __global__ void __launch_bounds__(kSplitThreads)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
+            const uint64_t wd0 = sdesc_sw128(smem_u32(base), 16, 1024);
+            const uint64_t xd0 = sdesc_sw128(smem_u32(base + kWBytes), 16, 1024);
             bool ok = true;
+            int s = 0;
+            uint32_t phase = 0;
             for (int k = 0; k < nk; ++k) {
-                const int s = k % stages;
-                if (!mbar_wait_bounded(&S.full[s], (k / stages) & 1, abort, status)) { ok = false; break; }
+                if (!mbar_wait_bounded(&S.full[s], phase, abort, status)) { ok = false; break; }
                 tc_fence_after();
-                const uint8_t* st = base + s * kStageBytes;
-                stage_mmas<1>(tbase, st, st + kWBytes, idesc_i8(kRows, NT), K - (k_begin + k) * kBK, k == 0);
+                stage_mmas<1>(tbase, wd0 + s * (kStageBytes >> 4), xd0 + s * (kStageBytes >> 4), idesc_i8(kRows, NT),
+                              K - (k_begin + k) * kBK, k == 0);
                 umma_commit(&S.empty[s]);
+                if (++s == stages) { s = 0; phase ^= 1; }
             }
             if (ok) umma_commit(&S.done);
         }
         __syncwarp();
     } else {
         // the partial sums to shared memory (the stages' place: they have
-        // been read), token by token; zeros where this CTA had no part of K
+        // been read), token by token
         const int q = warp & 3;
         int* part = reinterpret_cast<int*>(base);
         const int row = q * 32 + lane;
-        if (nk == 0 || mbar_wait_warp(&S.done, 0, abort, status)) {
+        if (row < NT) S.token[row] = token_scale(a, m0 + row);
+        if (mbar_wait_warp(&S.done, 0, abort, status)) {
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < NT; c += 16) {
-                float v[16] = {};
-                if (nk > 0) {
-                    tmem_ld_32x32b_x16(tbase + (static_cast<uint32_t>(q * 32) << 16) + c, v);
-                    tmem_ld_wait();
-                }
+                int v[16];
+                tmem_ld_cols(tbase + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+                tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = __float_as_int(v[j]);
+                for (int j = 0; j < 16; ++j) part[(c + j) * kRows + row] = v[j];
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    cluster::sync();
-    {   // this CTA's share of the tile: 4 neighbouring outputs a thread
-        const int rows = static_cast<int>(min(static_cast<int64_t>(NT), a.M - m0));
-        const int quads = rows * (kRows / 4);
-        const int q0 = quads * rank / splits, q1 = quads * (rank + 1) / splits;
-        for (int e = q0 + static_cast<int>(threadIdx.x); e < q1; e += kSplitThreads) {
-            const int64_t m = m0 + e / (kRows / 4);
-            const int64_t n = n0 + 4 * (e % (kRows / 4));
-            if (n >= a.N) continue;
-            int sum[4] = {0, 0, 0, 0};
-            for (int p = 0; p < splits; ++p) {
-                const int4 v = cluster::load_int4(cluster::map_address(base + 16 * e, p));
-                sum[0] += v.x;
-                sum[1] += v.y;
-                sum[2] += v.z;
-                sum[3] += v.w;
-            }
-            const uint2 t = token_scale(a, m);
-            T* y = static_cast<T*>(a.Y) + m * a.ldy + n;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + j < a.N) store_rounded(y + j, output(sum[j], row_scale(a, n + j), t));
-        }
-    }
-    cluster::sync();   // no CTA leaves while another reads its sums
+    cluster::arrive();
+    // freed before the cluster meets: a CTA that waits for others holds no
+    // tensor memory that they, or another kernel on their SMs, may wait for
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tbase, kCols);
     }
+    cluster::wait();
+    for (int t0 = tokens * rank / splits + warp; t0 < t_end; t0 += 2 * (kSplitThreads / 32)) {
+        // two tokens at a time: the loads of both are on their way together
+        int4 sum[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + i * (kSplitThreads / 32);
+            int4 v[kMaxSplits];
+#pragma unroll
+            for (int p = 0; p < kMaxSplits; ++p)
+                if (p < splits && t < t_end) v[p] = cluster::load_int4(cluster::map_address(base + 4 * (t * kRows + 4 * lane), p));
+            sum[i] = v[0];
+#pragma unroll
+            for (int p = 1; p < kMaxSplits; ++p)
+                if (p < splits && t < t_end) {
+                    sum[i].x += v[p].x;
+                    sum[i].y += v[p].y;
+                    sum[i].z += v[p].z;
+                    sum[i].w += v[p].w;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + i * (kSplitThreads / 32);
+            if (t >= t_end) continue;
+            const uint2 token = S.token[t];
+            store4(static_cast<T*>(a.Y) + (m0 + t) * a.ldy + n, a.N - n, output(sum[i].x, rows[0], token),
+                   output(sum[i].y, rows[1], token), output(sum[i].z, rows[2], token), output(sum[i].w, rows[3], token));
+        }
+    }
+    cluster::sync();   // no CTA leaves while another reads its sums
 }
 
 // -------------------------------------------------------------- few tokens
@@ -431,7 +539,6 @@ __global__ void __launch_bounds__(kSplitThreads)
 // tokens at 16 codes 16 t .. of each 64: two 8-code operands of two MMAs, the
 // same (permuted) order of K on both sides.  A row's 128 codes a step are read
 // in whole lines, U steps in flight a warp.
-constexpr int kFewWarps = 8;
 constexpr int kFewRows = 16;
 
 __device__ __forceinline__ uint4 load_once(const void* p)
@@ -463,10 +570,10 @@ __device__ __forceinline__ void mma_i8(int (&c)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int MT, int U, typename T>
-__global__ void __launch_bounds__(kFewWarps * 32) w8a8_few_kernel(const W8A8Args a)
+template <int MT, int U, int W, typename T>
+__global__ void __launch_bounds__(W * 32) w8a8_few_kernel(const W8A8Args a)
 {
-    __shared__ int part[kFewWarps][8 * MT][kFewRows];
+    __shared__ int part[W][8 * MT][kFewRows];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -480,13 +587,13 @@ __global__ void __launch_bounds__(kFewWarps * 32) w8a8_few_kernel(const W8A8Args
 #pragma unroll
     for (int j = 0; j < MT; ++j) x[j] = a.Xq + min(static_cast<int64_t>(8 * j + g), a.M - 1) * a.ldx;
     int acc[MT][4] = {};
-    for (int s = warp; s < steps; s += kFewWarps * U) {
+    for (int s = warp; s < steps; s += W * U) {
         uint4 w[U][2][2], xb[U][2][MT];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int k = (s + kFewWarps * u) * kBK + 64 * h + 16 * t;
+                const int k = (s + W * u) * kBK + 64 * h + 16 * t;
                 const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                 w[u][h][0] = k < K ? load_once(w0 + k) : zero;
                 w[u][h][1] = k < K ? load_once(w1 + k) : zero;
@@ -512,12 +619,12 @@ __global__ void __launch_bounds__(kFewWarps * 32) w8a8_few_kernel(const W8A8Args
         part[warp][8 * j + 2 * t + 1][g + 8] = acc[j][3];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 8 * MT * kFewRows; e += kFewWarps * 32) {
+    for (int e = threadIdx.x; e < 8 * MT * kFewRows; e += W * 32) {
         const int64_t m = e / kFewRows, n = n0 + e % kFewRows;
         if (m >= a.M || n >= a.N) continue;
         int sum = 0;
 #pragma unroll
-        for (int p = 0; p < kFewWarps; ++p) sum += part[p][m][e % kFewRows];
+        for (int p = 0; p < W; ++p) sum += part[p][m][e % kFewRows];
         store_rounded(static_cast<T*>(a.Y) + m * a.ldy + n, output(sum, row_scale(a, n), token_scale(a, m)));
     }
 }
@@ -591,15 +698,15 @@ int launch_pair(const W8A8Args& a, cudaStream_t stream)
 }
 
 template <int NT, typename T>
-int launch_split(const W8A8Args& a, cudaStream_t stream)
+int launch_split(const W8A8Args& a, int splits, cudaStream_t stream)
 {
     constexpr int stage_bytes = kWBytes + NT * kBK;
-    constexpr int max_stages = std::min(kMaxStages, 104 * 1024 / stage_bytes);   // two CTAs an SM
     const int n_tiles = static_cast<int>((a.N + kRows - 1) / kRows), m_tiles = static_cast<int>((a.M + NT - 1) / NT);
     const int blocks = static_cast<int>((a.K + kBK - 1) / kBK);
-    const int64_t tiles = static_cast<int64_t>(n_tiles) * m_tiles;
-    const int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({2 * sm_count() / tiles, kMaxSplits, blocks})));
-    const int stages = std::min(max_stages, (blocks + splits - 1) / splits);
+    // all of an SM's shared memory where each has one CTA at most, else half
+    // (clusters of more than 4 such CTAs do not all find their SMs in one GPC)
+    const bool alone = static_cast<int64_t>(n_tiles) * m_tiles * splits <= sm_count() && splits <= 4;
+    const int stages = std::min({kMaxStages, (alone ? 200 : 104) * 1024 / stage_bytes, (blocks + splits - 1) / splits});
     const int smem = std::max(stages * stage_bytes, NT * kRows * 4) + 1024;
     static int smem_set[64] = {};
     int rc = allow_smem(w8a8_split_kernel<NT, T>, smem_set, smem);
@@ -627,23 +734,92 @@ int launch_split(const W8A8Args& a, cudaStream_t stream)
     return GPTQ_OK;
 }
 
-template <int MT, int U, typename T>
+template <int MT, int U, int W, typename T>
 int launch_few(const W8A8Args& a, cudaStream_t stream)
 {
     const unsigned blocks = static_cast<unsigned>((a.N + kFewRows - 1) / kFewRows);
-    w8a8_few_kernel<MT, U, T><<<blocks, kFewWarps * 32, 0, stream>>>(a);
+    w8a8_few_kernel<MT, U, W, T><<<blocks, W * 32, 0, stream>>>(a);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
+}
+
+// Which kernel, and how it is cut.  The times are a model of what was measured
+// on B200 (us; M x N x K with bf16 out):
+//   few tokens: a block reads 16 weight rows and, again, every token's row.
+//     8 x 4096 x 4096 4.2 against 5.9 by the split kernel, 16 x 4096 x 4096 5.4
+//     against 6.3, 16 x 4096 x 11008 12.7 against 12.2, 24 x 1000 x 1003 3.8
+//     against 5.1, 24 x 1024 x 4096 5.2 against 5.5, 24 x 4096 x 4096 9.2
+//     against 6.3;
+//   tiles: a start and an end (longer for more tokens a tile and more CTAs than
+//     SMs), then whichever is longest of the issue of a CTA's stages, the operands' way from L2 (14
+//     bytes a ps over all SMs) and the weights' from memory (6.2, less with few CTAs).  128 x 4096 x 4096:
+//     split 128 9.3, split 64 9.7, pair 64 12.9; 256 x 4096 x 11008: split 128
+//     19.9, pair 128 24.0; 512 x 4096 x 4096: pair 128 14.2, pair 256 17.2,
+//     split 128 16.4; 1024 x 4096 x 4096: pair 256 18.1, pair 128 20.6;
+//     256 x 11008 x 4096: pair 256 19.1, pair 128 22.8, split 128 23.5;
+//     2048 x 1024 x 4096: pair 128 14.4, split 128 16.0.
+struct Choice {
+    int tokens;   // a tile's
+    int splits;   // CTAs that share a tile's K; 0: the pair kernel
+};
+
+Choice choose_tiles(int64_t M, int64_t N, int64_t K)
+{
+    const double sms = sm_count(), blocks = static_cast<double>((K + kBK - 1) / kBK);
+    Choice best{256, 0};
+    double best_time = 1e30;
+    auto consider = [&](Choice c, double ctas, double ends, double issue, double bytes) {
+        const double memory = static_cast<double>(N) * K / std::min(6.2e6, 0.056e6 * ctas);
+        const double t = ends + std::max({issue, bytes / 14e6, memory});
+        if (t < best_time) {
+            best_time = t;
+            best = c;
+        }
+    };
+    for (int nt : {32, 64, 128}) {
+        if (nt > 32 && nt / 2 >= M) break;   // half the tile would be empty
+        const int64_t tiles = (N + kRows - 1) / kRows * ((M + nt - 1) / nt);
+        // one CTA an SM while each keeps 4 stages of K, two while it keeps 8
+        const int64_t one = std::min<int64_t>(sm_count() / tiles, static_cast<int64_t>(blocks) / 4);
+        const int64_t two = std::min<int64_t>(2 * sm_count() / tiles, static_cast<int64_t>(blocks) / 8);
+        const int splits = static_cast<int>(std::min<int64_t>(kMaxSplits, std::max<int64_t>({1, one, two})));
+        const double own = std::ceil(blocks / splits);
+        const double rounds = std::ceil(static_cast<double>(tiles) * splits / (2 * sms));
+        const double ends = 3.5 + 0.008 * nt + 0.03 * nt / splits + 0.012 * std::max(0.0, tiles * splits - sms);
+        consider({nt, splits}, static_cast<double>(tiles) * splits, ends, rounds * own * 0.2,
+                 static_cast<double>(tiles) * splits * own * (kRows + nt) * kBK);
+    }
+    const struct { int nt; double ends, stage; } pairs[] = {{64, 4.9, 0.24}, {128, 5.6, 0.235}, {256, 7.5, 0.285}};
+    for (const auto& p : pairs) {
+        if (p.nt > 64 && p.nt / 2 >= M) break;
+        const int64_t tiles = (N + 2 * kRows - 1) / (2 * kRows) * ((M + p.nt - 1) / p.nt);
+        consider({p.nt, 0}, 2.0 * tiles, p.ends, std::ceil(2.0 * tiles / sms) * blocks * p.stage,
+                 static_cast<double>(tiles) * blocks * (2 * kRows + p.nt) * kBK);
+    }
+    return best;
 }
 
 template <typename T>
 int run_typed(const W8A8Args& a, cudaStream_t stream)
 {
-    if (a.M <= 8) return launch_few<1, 4, T>(a, stream);
-    if (a.M <= 16) return launch_few<2, 2, T>(a, stream);
-    if (a.M <= 32) return launch_split<32, T>(a, stream);
-    if (a.M <= 64) return launch_split<64, T>(a, stream);
-    if (a.M <= 128) return launch_split<128, T>(a, stream);
+    const int64_t weights = a.N * a.K;
+    if (a.M <= 8) {
+        // many blocks: four warps each and more blocks an SM, whose loads and
+        // reductions overlap (1 x 11008 x 4096 9.1 us against 10.8); else eight
+        // warps a block, each with more on its way (1 x 4096 x 4096 3.6 against 5.2)
+        if (a.N >= int64_t(3) * kFewRows * sm_count()) return launch_few<1, 2, 4, T>(a, stream);
+        return launch_few<1, 4, 8, T>(a, stream);
+    }
+    if (a.M <= 16 && weights <= (int64_t(1) << 25)) return launch_few<2, 2, 8, T>(a, stream);
+    if (a.M <= 32 && weights <= (int64_t(1) << 22)) return launch_few<4, 2, 8, T>(a, stream);
+    const Choice c = choose_tiles(a.M, a.N, a.K);
+    if (c.splits) {
+        if (c.tokens == 32) return launch_split<32, T>(a, c.splits, stream);
+        if (c.tokens == 64) return launch_split<64, T>(a, c.splits, stream);
+        return launch_split<128, T>(a, c.splits, stream);
+    }
+    if (c.tokens == 64) return launch_pair<64, T>(a, stream);
+    if (c.tokens == 128) return launch_pair<128, T>(a, stream);
     return launch_pair<256, T>(a, stream);
 }
 
