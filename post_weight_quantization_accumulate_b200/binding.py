@@ -323,31 +323,36 @@ def gptq_w4a16_gemm(Y: torch.Tensor, X: torch.Tensor, packed: torch.Tensor, scal
                                  _ptr(g_idx), M, N, K, group_size, path, _stream(Y, stream)))
 
 
-def _rows(t, dtype, shape, name):
-    """(address, row pitch) of a matrix whose rows are contiguous; (None, 0) for None."""
-    if t is None:
-        return None, 0
+def _refuse(t, dtype, shape, dev, name):
+    """Says what is wrong with an argument that _rows or _vec does not take."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
+    if t.get_device() != dev:
+        raise ValueError("tensor arguments must be on one device")
+    raise ValueError(f"the rows of {name} must be contiguous")
+
+
+def _rows(t, dtype, shape, dev, name):
+    """(address, row pitch) of a matrix whose rows are contiguous; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, dtype, shape, dev, name)
     pitch, step = t.stride()
     if step != 1 and shape[1] > 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
+        _refuse(t, dtype, shape, dev, name)
     # the pitch of a single row is not looked at: any that the library accepts
     return t.data_ptr(), pitch if shape[0] > 1 else (shape[1] + 15) // 16 * 16
 
 
-def _vec(t, dtype, n, name):
-    """Address of a contiguous vector of n elements; None for None."""
+def _vec(t, dtype, shape, dev, name):
+    """Address of a contiguous vector; None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.shape != (n,):
-        raise ValueError(f"{name} must be [{n}]")
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, shape, dev, name)
     return t.data_ptr()
 
 
@@ -364,21 +369,17 @@ def _type(t, name):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call_on(fn: str, t: torch.Tensor, others, stream, *args):
-    """Calls `fn` with the device of `t` current, on `stream` or that device's
-    current stream; every other tensor has to be on the same device."""
-    device = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != device:
-            raise ValueError("tensor arguments must be on one device")
-    if device < 0:
+def _call_on(fn: str, dev: int, t: torch.Tensor, stream, *args):
+    """Calls `fn` with device `dev` (that of t) current, on `stream` or the
+    device's current stream."""
+    if dev < 0:
         raise ValueError("tensor arguments must be on a CUDA device")
     f = getattr(_lib or lib(), fn)
-    s = _raw_stream(device) if stream is None and _raw_stream else _stream(t, stream)
-    if device == torch.cuda.current_device():
+    s = _raw_stream(dev) if stream is None and _raw_stream else _stream(t, stream)
+    if dev == torch.cuda.current_device():
         st = f(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             st = f(*args, s)
     if st != GPTQ_OK:
         raise GptqError(fn, st)
@@ -391,14 +392,14 @@ def gptq_quantize_tokens(Xq: torch.Tensor | None, x_scales: torch.Tensor, x_sums
     x_sums (int32 [M]) and hat ([M, K], X's type) are outputs: the 8-bit
     tokens of X, or of silu(gate) * X."""
     ty = _type(X, "X")
-    M, K = X.shape
-    q, ldq = _rows(Xq, torch.int8, X.shape, "Xq")
-    h, ldh = _rows(hat, X.dtype, X.shape, "hat")
-    x, ldx = _rows(X, X.dtype, X.shape, "X")
-    g, ldg = _rows(gate, X.dtype, X.shape, "gate")
-    _call_on("gptq_quantize_tokens", X, (Xq, x_scales, x_sums, gate, hat), stream, q, ldq,
-             _vec(x_scales, torch.float32, M, "x_scales"), _vec(x_sums, torch.int32, M, "x_sums"), h, ldh,
-             x, ldx, g, ldg, ty, M, K)
+    shape, dev, dtype = X.shape, X.get_device(), X.dtype
+    M, K = shape
+    q, ldq = _rows(Xq, torch.int8, shape, dev, "Xq")
+    h, ldh = _rows(hat, dtype, shape, dev, "hat")
+    x, ldx = _rows(X, dtype, shape, dev, "X")
+    g, ldg = _rows(gate, dtype, shape, dev, "gate")
+    _call_on("gptq_quantize_tokens", dev, X, stream, q, ldq, _vec(x_scales, torch.float32, (M,), dev, "x_scales"),
+             _vec(x_sums, torch.int32, (M,), dev, "x_sums"), h, ldh, x, ldx, g, ldg, ty, M, K)
 
 
 def gptq_block_norm(block: torch.Tensor | None, residual: torch.Tensor | None,
@@ -412,21 +413,20 @@ def gptq_block_norm(block: torch.Tensor | None, residual: torch.Tensor | None,
     D]), q_scales, q_sums are outputs; those not given are not computed."""
     t = block if block is not None else residual
     ty = _type(t, "block" if block is not None else "residual")
-    M, D = t.shape
-    so, lds = _rows(stream_out, t.dtype, t.shape, "stream_out")
-    o, ldo = _rows(out, t.dtype, t.shape, "out")
-    qp, ldq = _rows(q, torch.int8, t.shape, "q")
-    b, ldb = _rows(block, t.dtype, t.shape, "block")
-    r, ldr = _rows(residual, t.dtype, t.shape, "residual")
+    shape, dev, dtype = t.shape, t.get_device(), t.dtype
+    M, D = shape
+    so, lds = _rows(stream_out, dtype, shape, dev, "stream_out")
+    o, ldo = _rows(out, dtype, shape, dev, "out")
+    qp, ldq = _rows(q, torch.int8, shape, dev, "q")
+    b, ldb = _rows(block, dtype, shape, dev, "block")
+    r, ldr = _rows(residual, dtype, shape, dev, "residual")
     if gate is not None and gate_rows < 1:
         raise ValueError("gate_rows must be positive")
-    g, ldg = _rows(gate, t.dtype, (-(-M // gate_rows) if gate is not None else 0, D), "gate")
-    _call_on("gptq_block_norm", t, (stream_out, out, q, q_scales, q_sums, block, residual, gate, post_weight,
-                                    pre_weight), stream, so, lds, o, ldo, qp, ldq,
-             _vec(q_scales, torch.float32, M, "q_scales"), _vec(q_sums, torch.int32, M, "q_sums"), b, ldb, r, ldr,
-             g, ldg, gate_rows, _vec(post_weight, torch.float32, D, "post_weight"),
-             _vec(pre_weight, torch.float32, D, "pre_weight"), int(bool(post_norm)), float(scale), float(eps),
-             ty, M, D)
+    g, ldg = _rows(gate, dtype, (-(-M // gate_rows), D), dev, "gate") if gate is not None else (None, 0)
+    _call_on("gptq_block_norm", dev, t, stream, so, lds, o, ldo, qp, ldq,
+             _vec(q_scales, torch.float32, (M,), dev, "q_scales"), _vec(q_sums, torch.int32, (M,), dev, "q_sums"),
+             b, ldb, r, ldr, g, ldg, gate_rows, _vec(post_weight, torch.float32, (D,), dev, "post_weight"),
+             _vec(pre_weight, torch.float32, (D,), dev, "pre_weight"), int(bool(post_norm)), scale, eps, ty, M, D)
 
 
 def gptq_w8a8_pack(Wq: torch.Tensor, w_zeros: torch.Tensor, codes: torch.Tensor, zeros: torch.Tensor, stream=None):
@@ -434,9 +434,10 @@ def gptq_w8a8_pack(Wq: torch.Tensor, w_zeros: torch.Tensor, codes: torch.Tensor,
     from the quantizer's 8-bit codes (uint8 [N, K]) and zeros (float32 [N])."""
     _need(codes, torch.uint8, "codes")
     N, K = codes.shape
-    w, ldw = _rows(Wq, torch.int8, codes.shape, "Wq")
-    _call_on("gptq_w8a8_pack", codes, (Wq, w_zeros, zeros), stream, w, ldw, _vec(w_zeros, torch.int32, N, "w_zeros"),
-             _ptr(codes), _vec(zeros, torch.float32, N, "zeros"), N, K)
+    dev = codes.get_device()
+    w, ldw = _rows(Wq, torch.int8, codes.shape, dev, "Wq")
+    _call_on("gptq_w8a8_pack", dev, codes, stream, w, ldw, _vec(w_zeros, torch.int32, (N,), dev, "w_zeros"),
+             _ptr(codes), _vec(zeros, torch.float32, (N,), dev, "zeros"), N, K)
 
 
 def gptq_w8a8_gemm(Y: torch.Tensor, Xq: torch.Tensor, x_scales: torch.Tensor, Wq: torch.Tensor,
@@ -449,15 +450,15 @@ def gptq_w8a8_gemm(Y: torch.Tensor, Xq: torch.Tensor, x_scales: torch.Tensor, Wq
     _need(Wq, torch.int8, "Wq")
     M, K = Xq.shape
     N = Wq.shape[0]
+    dev = Y.get_device()
     if w_zeros is not None and x_sums is None:
         raise ValueError("weights with a zero point need x_sums")
-    y, ldy = _rows(Y, Y.dtype, (M, N), "Y")
-    x, ldx = _rows(Xq, torch.int8, (M, K), "Xq")
-    w, ldw = _rows(Wq, torch.int8, (N, K), "Wq")
-    _call_on("gptq_w8a8_gemm", Y, (Xq, x_scales, Wq, w_scales, x_sums, w_zeros, bias), stream, y, ldy, ty, x, ldx,
-             _vec(x_scales, torch.float32, M, "x_scales"), _vec(x_sums, torch.int32, M, "x_sums"), w, ldw,
-             _vec(w_scales, torch.float32, N, "w_scales"), _vec(w_zeros, torch.int32, N, "w_zeros"),
-             _vec(bias, torch.float32, N, "bias"), M, N, K)
+    y, ldy = _rows(Y, Y.dtype, (M, N), dev, "Y")
+    x, ldx = _rows(Xq, torch.int8, (M, K), dev, "Xq")
+    w, ldw = _rows(Wq, torch.int8, (N, K), dev, "Wq")
+    _call_on("gptq_w8a8_gemm", dev, Y, stream, y, ldy, ty, x, ldx, _vec(x_scales, torch.float32, (M,), dev, "x_scales"),
+             _vec(x_sums, torch.int32, (M,), dev, "x_sums"), w, ldw, _vec(w_scales, torch.float32, (N,), dev, "w_scales"),
+             _vec(w_zeros, torch.int32, (N,), dev, "w_zeros"), _vec(bias, torch.float32, (N,), dev, "bias"), M, N, K)
 
 
 def gptq_bf16_to_f32(dst: torch.Tensor, src: torch.Tensor, stream=None):
