@@ -1,9 +1,11 @@
-"""Builds libgptq.so (sm_100a) in-tree from csrc/*.cu with nvcc.
+"""Builds libgptq.so (sm_100a) in-tree from csrc/*.cu with nvcc, and the
+CPython module _calls.so (the host side of w8a8.py) from csrc/calls.cpp with
+the C++ compiler.
 
     python -m post_weight_quantization_accumulate_b200.build [--force] [--verbose]
 
-Objects go to _build/ at the repository root; the library lands next to this
-file so it travels with the source tree.
+Objects go to _build/ at the repository root; the libraries land next to this
+file so they travel with the source tree.
 """
 from __future__ import annotations
 
@@ -14,12 +16,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgptq.so")
+CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -41,15 +46,43 @@ def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "gptq.h")]
 
 
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps())
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """_calls.so: torch's headers and libraries, and libgptq.so beside it."""
+    if not force and _newer(CALLS, [CALLS_SRC, os.path.join(ROOT, "include", "gptq.h")]):
+        return CALLS
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", tmp, "-L", PKG, "-lgptq", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           # the C++ runtime that torch has loaded, not a copy of its own: streams of a second,
+           # static one crashed where torch's had set up the locale
+           "-nostdlib++", "-l:libstdc++.so.6", "-Wl,-rpath," + os.path.join(base, "lib")]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and up_to_date():
+        build_calls(force, verbose)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -78,6 +111,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_calls(force, verbose)
     return LIB
 
 

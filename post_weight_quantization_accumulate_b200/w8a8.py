@@ -4,15 +4,37 @@ The consumer of `LayerQuantizer(..., bits=8, group_size=-1)`: its codes, laid
 out once as a `Weight`, are multiplied with activations that are quantized a
 token at a time, by themselves (`quantize_tokens`), after a gated activation
 (`gate`) or as the output of the norm between two blocks (`block_norm`).  All
-arithmetic happens in libgptq.so; this module allocates the outputs.
+arithmetic happens in libgptq.so; the calls here allocate their outputs, run
+on the current stream of the inputs' device and can be captured into graphs.
+They go through _calls.so, which does in C++ what the gptq_* functions of
+`binding` (for outputs of one's own, in place, or on a stream by argument) do
+in Python.
 """
 from __future__ import annotations
 
+import os
 from dataclasses import dataclass
 
 import torch
 
 from . import binding as B
+
+
+_native = None
+
+
+def _calls():
+    """The loaded _calls module (raises if it has not been built)."""
+    global _native
+    if _native is None:
+        B.lib()
+        if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_calls.so")):
+            raise RuntimeError("_calls.so is missing: build it with "
+                               "python -m post_weight_quantization_accumulate_b200.build")
+        from . import _calls as native
+        native.set_check(B._check)
+        _native = native
+    return _native
 
 
 @dataclass
@@ -51,13 +73,7 @@ def quantize_tokens(x: torch.Tensor, gate: torch.Tensor | None = None, codes: bo
                     hat: bool = False) -> Tokens:
     """The 8-bit tokens of x [M, K], or of silu(gate) * x; with `hat` also the
     values they stand for, in x's type."""
-    M, K = x.shape
-    t = Tokens(empty_codes(M, K, x.device) if codes else None,
-               torch.empty(M, dtype=torch.float32, device=x.device),
-               torch.empty(M, dtype=torch.int32, device=x.device),
-               torch.empty(M, K, dtype=x.dtype, device=x.device) if hat else None)
-    B.gptq_quantize_tokens(t.codes, t.scales, t.sums, x, gate, t.hat)
-    return t
+    return Tokens(*(_native or _calls()).quantize_tokens(x, gate, codes, hat))
 
 
 def block_norm(block: torch.Tensor | None, residual: torch.Tensor | None, pre_weight: torch.Tensor | None = None, *,
@@ -67,25 +83,13 @@ def block_norm(block: torch.Tensor | None, residual: torch.Tensor | None, pre_we
     """(r', out) with r' = residual + scale * gate * norm(block) and out =
     norm(r'); with `quantize` out is `Tokens`.  Without `keep_stream` r', and
     without `keep_out` out, is None and not stored.  See gptq_block_norm."""
-    x = block if block is not None else residual
-    M, D = x.shape
-    stream_out = torch.empty(M, D, dtype=x.dtype, device=x.device) if keep_stream else None
-    t, outs = None, {}
-    if keep_out and quantize:
-        t = Tokens(empty_codes(M, D, x.device), torch.empty(M, dtype=torch.float32, device=x.device),
-                   torch.empty(M, dtype=torch.int32, device=x.device))
-        outs = {"q": t.codes, "q_scales": t.scales, "q_sums": t.sums}
-    elif keep_out:
-        t = torch.empty(M, D, dtype=x.dtype, device=x.device)
-        outs = {"out": t}
-    B.gptq_block_norm(block, residual, pre_weight, stream_out=stream_out, post_norm=post_norm, post_weight=post_weight,
-                      gate=gate, gate_rows=gate_rows, scale=scale, eps=eps, **outs)
-    return stream_out, t
+    r, out, codes, scales, sums = (_native or _calls()).block_norm(
+        block, residual, pre_weight, post_norm, post_weight, gate, gate_rows, scale, eps, quantize, keep_stream, keep_out)
+    return r, (Tokens(codes, scales, sums) if codes is not None else out)
 
 
 def linear(tokens: Tokens, weight: Weight, bias: torch.Tensor | None = None,
            dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """Y [M, N] of the given type: the tokens times the weights transposed."""
-    y = torch.empty(tokens.codes.shape[0], weight.codes.shape[0], dtype=dtype, device=tokens.codes.device)
-    B.gptq_w8a8_gemm(y, tokens.codes, tokens.scales, weight.codes, weight.scales, tokens.sums, weight.zeros, bias)
-    return y
+    return (_native or _calls()).linear(tokens.codes, tokens.scales, tokens.sums, weight.codes, weight.scales, weight.zeros,
+                                        bias, dtype)

@@ -417,6 +417,34 @@ def test_empty_calls():
     _done()
 
 
+def test_calls_refuse_what_does_not_fit():
+    x = torch.zeros(3, 50, dtype=BF16, device="cuda")
+    t = w8a8.quantize_tokens(x)
+    w = w8a8.Weight(w8a8.empty_codes(7, 50, "cuda").zero_(), torch.ones(7, device="cuda"),
+                    torch.zeros(7, dtype=torch.int32, device="cuda"))
+    for call in (lambda: w8a8.quantize_tokens(x.double()), lambda: w8a8.quantize_tokens(x, gate=x.float()),
+                 lambda: w8a8.block_norm(x, x.float()), lambda: w8a8.linear(t, w, dtype=torch.int8),
+                 lambda: w8a8.linear(t, w8a8.Weight(w.codes, w.scales.double())),
+                 lambda: w8a8.block_norm(x, x, torch.ones(50, dtype=BF16, device="cuda"))):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: w8a8.quantize_tokens(x.t()), lambda: w8a8.quantize_tokens(x, gate=x[:2]),
+                 lambda: w8a8.quantize_tokens(x.cpu()), lambda: w8a8.quantize_tokens(x, gate=x.cpu()),
+                 lambda: w8a8.block_norm(x, x, gate=x[:1], gate_rows=2), lambda: w8a8.block_norm(x, x, gate=x[:1]),
+                 lambda: w8a8.block_norm(x, x[:, :49]), lambda: w8a8.linear(t, w8a8.Weight(w.codes[:, :49], w.scales)),
+                 lambda: w8a8.linear(w8a8.Tokens(t.codes, t.scales), w), lambda: w8a8.linear(t, w, bias=torch.ones(6, device="cuda")),
+                 lambda: w8a8.linear(t, w8a8.Weight(w.codes, w.scales.cpu()))):
+        with pytest.raises(ValueError):
+            call()
+    # rows of 50 codes: not a pitch of 16 bytes, which the library refuses
+    for call in (lambda: w8a8.linear(t, w8a8.Weight(w.codes.contiguous(), w.scales)),
+                 lambda: w8a8.quantize_tokens(torch.zeros(1, 65537, dtype=BF16, device="cuda"))):
+        with pytest.raises(B.GptqError):
+            call()
+    assert torch.cuda.current_stream().query() in (True, False)
+    _done()
+
+
 # -- together ----------------------------------------------------------------------
 
 @pytest.mark.parametrize("N,K", [(7, 8), (130, 72), (256, 1024)])

@@ -119,3 +119,19 @@ def test_pack_needs_one_group_a_row():
 def test_calibrate_refuses_other_activation_widths():
     with pytest.raises(ValueError):
         decoder.calibrate(torch.zeros(8, 8), {}, decoder.TINY, act_bits=4)
+
+
+def test_calls_refuse_other_tensors(lib):
+    """The calls that allocate their outputs refuse what is not a matrix on a
+    GPU before they allocate or launch anything."""
+    x = torch.zeros(3, 50, dtype=torch.bfloat16)
+    t = w8a8.Tokens(w8a8.empty_codes(3, 50, "cpu"), torch.zeros(3))
+    w = w8a8.Weight(w8a8.empty_codes(7, 50, "cpu"), torch.zeros(7))
+    for call in (lambda: w8a8.quantize_tokens(x), lambda: w8a8.block_norm(x, x), lambda: w8a8.linear(t, w),
+                 lambda: w8a8.quantize_tokens(x[0])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: w8a8.quantize_tokens(None), lambda: w8a8.block_norm(None, None),
+                 lambda: w8a8.linear(w8a8.Tokens(None, torch.zeros(3)), w)):
+        with pytest.raises(TypeError):
+            call()
