@@ -254,49 +254,70 @@ __device__ __forceinline__ float2 silu(float2 a)
     return mul2(a, make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y)));
 }
 
-__device__ __forceinline__ float warp_sum(float v)
+// The threads of a row: whole warps, or (SHORT) 8 or 16 neighbouring lanes.
+template <bool SHORT>
+struct RowThreads {
+    int threads;   // of a row
+    int tid;       // this thread's place among them
+    int row;       // the block's row
+
+    __device__ explicit RowThreads(int threads_)
+        : threads(threads_), tid(threadIdx.x % threads_), row(threadIdx.x / threads_) {}
+    __device__ int warps() const { return SHORT ? 1 : threads / 32; }
+    __device__ int width() const { return SHORT ? threads : 32; }
+    __device__ int lane() const { return tid & (width() - 1); }
+    __device__ uint32_t lanes() const
+    {
+        return SHORT ? ((1u << threads) - 1u) << ((threadIdx.x & 31) & ~(threads - 1)) : 0xffffffffu;
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v, int width = 32)
 {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o; o >>= 1)
+        if (o < width) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// Over the `warps` warps of a row, the block's row-th.  Each reduction of a
-// kernel has slots of its own, so that one barrier each is enough.  A block
-// has several rows only where they have four warps at most.
-__device__ __forceinline__ int row_slot(int row, int warps) { return warps <= 4 ? 4 * row : 0; }
+// Over the threads of a row.  Each reduction of a kernel has slots of its own,
+// so that one barrier each is enough.  A block has several rows only where
+// they have four warps at most.
+template <bool SHORT>
+__device__ __forceinline__ int row_slot(const RowThreads<SHORT>& r) { return r.warps() <= 4 ? 4 * r.row : 0; }
 
-__device__ __forceinline__ float row_sum(float v, float (&part)[32], int row, int warps, int warp)
+template <bool SHORT>
+__device__ __forceinline__ float row_sum(float v, float (&part)[32], const RowThreads<SHORT>& r)
 {
-    v = warp_sum(v);
+    v = warp_sum(v, r.width());
+    const int warps = r.warps();
     if (warps == 1) return v;
-    const int lane = threadIdx.x & 31;
-    const float* p = part + row_slot(row, warps);
-    if (lane == 0) part[row_slot(row, warps) + warp] = v;
+    const float* p = part + row_slot(r);
+    if (r.lane() == 0) part[row_slot(r) + (r.tid >> 5)] = v;
     __syncthreads();
     if (warps <= 4) return (p[0] + p[1]) + (warps > 2 ? p[2] + (warps > 3 ? p[3] : 0.f) : 0.f);
-    return warp_sum(lane < warps ? p[lane] : 0.f);
+    return warp_sum(r.lane() < warps ? p[r.lane()] : 0.f);
 }
 
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (&part)[32], int row, int warps, int warp)
+template <bool SHORT>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (&part)[32], const RowThreads<SHORT>& r)
 {
-    v = __reduce_max_sync(0xffffffffu, v);
-    if (warps == 1) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) part[row_slot(row, warps) + warp] = v;
+    v = __reduce_max_sync(r.lanes(), v);
+    if (r.warps() == 1) return v;
+    if (r.lane() == 0) part[row_slot(r) + (r.tid >> 5)] = v;
     __syncthreads();
-    return __reduce_max_sync(0xffffffffu, lane < warps ? part[row_slot(row, warps) + lane] : 0u);
+    return __reduce_max_sync(0xffffffffu, r.lane() < r.warps() ? part[row_slot(r) + r.lane()] : 0u);
 }
 
 // The sum ends up with the row's first warp.
-__device__ __forceinline__ int row_sum_first(int v, int (&part)[32], int row, int warps, int warp)
+template <bool SHORT>
+__device__ __forceinline__ int row_sum_first(int v, int (&part)[32], const RowThreads<SHORT>& r)
 {
-    v = __reduce_add_sync(0xffffffffu, v);
-    if (warps == 1) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) part[row_slot(row, warps) + warp] = v;
+    v = __reduce_add_sync(r.lanes(), v);
+    if (r.warps() == 1) return v;
+    if (r.lane() == 0) part[row_slot(r) + (r.tid >> 5)] = v;
     __syncthreads();
-    return warp == 0 ? __reduce_add_sync(0xffffffffu, lane < warps ? part[row_slot(row, warps) + lane] : 0) : 0;
+    return r.tid < 32 ? __reduce_add_sync(0xffffffffu, r.lane() < r.warps() ? part[row_slot(r) + r.lane()] : 0) : 0;
 }
 
 // ------------------------------------------------------------------ codes
@@ -410,12 +431,12 @@ __device__ __forceinline__ uint32_t pack4(float2 a, float2 b)
 }
 
 // Stores the codes of the chunk at k (elements not there have code 0) and
-// returns their sum.  Called by whole warps, whose lanes hold neighbouring
-// chunks.  Off the boundaries of the codes' row a lane stores the word that
-// its chunk shares with the next lane's; at the warp's ends, and at the row's,
-// single codes.
-template <typename T, bool SHIFT>
-__device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live, const Chunk<T>& c)
+// returns their sum.  Called by whole warps; a row's lanes in a warp hold
+// neighbouring chunks.  Off the boundaries of the codes' row a lane stores the
+// word that its chunk shares with the next lane's; at the ends of a row's lanes
+// in the warp, and of the row, single codes.
+template <typename T, bool SHIFT, bool SHORT>
+__device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live, const Chunk<T>& c, const RowThreads<SHORT>& r)
 {
     constexpr int VEC = kVec<T>;
     uint32_t w[VEC / 4];
@@ -445,10 +466,9 @@ __device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live,
         uint64_t next = 0;
         if (lead) next = __shfl_down_sync(0xffffffffu, own, 1);
         if (live && k < K) {
-            const int lane = threadIdx.x & 31;
-            if (lead && lane == 0) put(own << (8 * (VEC - lead)), k + lead - VEC, VEC - lead, VEC);
+            if (lead && r.lane() == 0) put(own << (8 * (VEC - lead)), k + lead - VEC, VEC - lead, VEC);
             const uint64_t word = lead ? own >> (8 * lead) | next << (8 * (VEC - lead)) : own;
-            put(word, k + lead, 0, lead && lane == 31 ? VEC - lead : VEC);
+            put(word, k + lead, 0, lead && r.lane() == r.width() - 1 ? VEC - lead : VEC);
         }
     }
     return sum;
@@ -487,14 +507,15 @@ struct TokenArgs {
 template <typename T, int CH>
 constexpr int max_row_threads() { return kHeldCols / (kVec<T> * CH) < 1024 ? kHeldCols / (kVec<T> * CH) : 1024; }
 
-template <typename T, int CH, bool SHIFT, bool GATE>
-__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) quantize_tokens_kernel(const TokenArgs a, int warps)
+template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT>
+__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) quantize_tokens_kernel(const TokenArgs a, int threads)
 {
     constexpr int VEC = kVec<T>;
     __shared__ uint32_t part_top[32];
     __shared__ int part_sum[32];
-    const int tid = threadIdx.x % (32 * warps), row = threadIdx.x / (32 * warps), warp = tid >> 5;
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (32 * warps)) + row;
+    const RowThreads<SHORT> row(threads);
+    const int tid = row.tid;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / threads) + row.row;
     const bool live = m < a.M;
     const T* x = static_cast<const T*>(a.X) + m * a.ldx;
     const T* gate = static_cast<const T*>(a.gate) + m * a.ldg;
@@ -507,8 +528,8 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
     uint4 xr[CH], gr[GATE ? CH : 1];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        xr[i] = load_chunk<T, SHIFT>(x, k0 + i * 32 * warps * VEC, a.K, live);
-        if (GATE) gr[i] = load_chunk<T, SHIFT>(gate, k0 + i * 32 * warps * VEC, a.K, live);
+        xr[i] = load_chunk<T, SHIFT>(x, k0 + i * threads * VEC, a.K, live);
+        if (GATE) gr[i] = load_chunk<T, SHIFT>(gate, k0 + i * threads * VEC, a.K, live);
     }
     // what is kept through the reduction: 16-bit values as they are, else float32
     constexpr bool PACKED = !GATE && sizeof(T) == 2;
@@ -536,15 +557,15 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
         top = max(__float_as_uint(two.x), __float_as_uint(two.y));
     }
     constexpr bool ELEVEN = PACKED && std::is_same<T, __half>::value;
-    const TokenGrid g = token_grid<ELEVEN>(row_max(top, part_top, row, warps, warp));
+    const TokenGrid g = token_grid<ELEVEN>(row_max(top, part_top, row));
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int k = k0 + i * 32 * warps * VEC;
+        const int k = k0 + i * threads * VEC;
         Chunk<T>& w = v[PACKED ? 0 : i];
         if constexpr (PACKED) w = widen_chunk<T>(xr[i]);
         code_chunk<T, ELEVEN, !GATE && sizeof(T) == 4>(w, g);
-        sum += store_codes<T, SHIFT>(a.Xq ? a.Xq + m * a.ldq : nullptr, k, a.K, live, w);
+        sum += store_codes<T, SHIFT>(a.Xq ? a.Xq + m * a.ldq : nullptr, k, a.K, live, w, row);
         if (a.hat && live && k < a.K) {
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) w.v[j] = mul2(add2(w.v[j], both(-kRound)), both(g.scale));
@@ -552,21 +573,22 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
         }
     }
     if (a.x_sums) {
-        sum = row_sum_first(sum, part_sum, row, warps, warp);
+        sum = row_sum_first(sum, part_sum, row);
         if (live && tid == 0) a.x_sums[m] = sum;
     }
     if (live && tid == 0) a.x_scales[m] = g.scale;
 }
 
-template <typename T, int CH, bool SHIFT, bool GATE>
-__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) block_norm_kernel(const BlockNormArgs a, int warps)
+template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT>
+__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) block_norm_kernel(const BlockNormArgs a, int threads)
 {
     constexpr int VEC = kVec<T>;
     __shared__ float part_post[32], part_pre[32];
     __shared__ uint32_t part_top[32];
     __shared__ int part_sum[32];
-    const int tid = threadIdx.x % (32 * warps), row = threadIdx.x / (32 * warps), warp = tid >> 5;
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (32 * warps)) + row;
+    const RowThreads<SHORT> row(threads);
+    const int tid = row.tid;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * (blockDim.x / threads) + row.row;
     const bool live = m < a.M;
     const int D = static_cast<int>(a.D);
     const T* block = static_cast<const T*>(a.block) + m * a.ldb;
@@ -575,7 +597,7 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
     T* stream_out = static_cast<T*>(a.stream_out) + m * a.lds;
     T* out = static_cast<T*>(a.out) + m * a.ldo;
     const int k0 = tid * VEC - (SHIFT ? lead_of<T>(a.stream_out ? stream_out : a.out ? out : a.block ? block : residual) : 0);
-    const int step = 32 * warps * VEC;
+    const int step = threads * VEC;
     if (tid == 0 && a.ahead && m + a.ahead < a.M) {
         if (a.block) prefetch_row(static_cast<const T*>(a.block), a.ldb, m + a.ahead, D);
         if (a.residual) prefetch_row(static_cast<const T*>(a.residual), a.ldr, m + a.ahead, D);
@@ -597,7 +619,7 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) s = fma2(c.v[j], c.v[j], s);
         }
-        scale *= rsqrtf(row_sum(s.x + s.y, part_post, row, warps, warp) / static_cast<float>(D) + a.eps);
+        scale *= rsqrtf(row_sum(s.x + s.y, part_post, row) / static_cast<float>(D) + a.eps);
     }
     Chunk<T> h[CH];
     float2 s = both(0.f);
@@ -628,7 +650,7 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
         }
     }
     if (!a.out && !a.q) return;
-    const float pre = rsqrtf(row_sum(s.x + s.y, part_pre, row, warps, warp) / static_cast<float>(D) + a.eps);
+    const float pre = rsqrtf(row_sum(s.x + s.y, part_pre, row) / static_cast<float>(D) + a.eps);
     if (a.out) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
@@ -641,15 +663,15 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
     }
     if (!a.q) return;
     // the codes are those of r' w: the factor rsqrt(...) of the row cancels in 127 v / t
-    const TokenGrid g = token_grid<false>(row_max(top, part_top, row, warps, warp));
+    const TokenGrid g = token_grid<false>(row_max(top, part_top, row));
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         code_chunk<T, false, false>(h[i], g);
-        sum += store_codes<T, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i]);
+        sum += store_codes<T, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i], row);
     }
     if (a.q_sums) {
-        sum = row_sum_first(sum, part_sum, row, warps, warp);
+        sum = row_sum_first(sum, part_sum, row);
         if (live && tid == 0) a.q_sums[m] = sum;
     }
     if (live && tid == 0) a.q_scales[m] = g.scale * pre;
@@ -664,7 +686,7 @@ __global__ void __launch_bounds__(kWideThreads) quantize_wide_tokens_kernel(cons
     __shared__ uint32_t part_top[32];
     __shared__ int part_sum[32];
     const int64_t m = blockIdx.x;
-    const int warps = kWideThreads / 32, warp = threadIdx.x >> 5;
+    const RowThreads<false> row(kWideThreads);
     const T* x = static_cast<const T*>(a.X) + m * a.ldx;
     const T* gate = a.gate ? static_cast<const T*>(a.gate) + m * a.ldg : nullptr;
     auto value = [&](int k) {
@@ -673,7 +695,7 @@ __global__ void __launch_bounds__(kWideThreads) quantize_wide_tokens_kernel(cons
     };
     uint32_t top = 0;
     for (int k = threadIdx.x; k < a.K; k += kWideThreads) top = max(top, magnitude(value(k)));
-    top = row_max(top, part_top, 0, warps, warp);
+    top = row_max(top, part_top, row);
     const TokenGrid g = gate ? token_grid<false>(top) : token_grid<std::is_same<T, __half>::value>(top);
     int sum = 0;
     for (int k = threadIdx.x; k < a.K; k += kWideThreads) {
@@ -685,7 +707,7 @@ __global__ void __launch_bounds__(kWideThreads) quantize_wide_tokens_kernel(cons
         if (a.hat) store_rounded(static_cast<T*>(a.hat) + m * a.ldh + k, q * g.scale);
     }
     if (a.x_sums) {
-        sum = row_sum_first(sum, part_sum, 0, warps, warp);
+        sum = row_sum_first(sum, part_sum, row);
         if (threadIdx.x == 0) a.x_sums[m] = sum;
     }
     if (threadIdx.x == 0) a.x_scales[m] = g.scale;
@@ -698,7 +720,7 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const Blo
     __shared__ uint32_t part_top[32];
     __shared__ int part_sum[32];
     const int64_t m = blockIdx.x;
-    const int warps = kWideThreads / 32, warp = threadIdx.x >> 5;
+    const RowThreads<false> row(kWideThreads);
     const int D = static_cast<int>(a.D);
     const T* block = a.block ? static_cast<const T*>(a.block) + m * a.ldb : nullptr;
     const T* residual = a.residual ? static_cast<const T*>(a.residual) + m * a.ldr : nullptr;
@@ -710,7 +732,7 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const Blo
             const float h = load_as_f32(block + k);
             s = fmaf(h, h, s);
         }
-        scale *= rsqrtf(row_sum(s, part_post, 0, warps, warp) / static_cast<float>(D) + a.eps);
+        scale *= rsqrtf(row_sum(s, part_post, row) / static_cast<float>(D) + a.eps);
     }
     auto value = [&](int k) {
         const float r = residual ? load_as_f32(residual + k) : 0.f;
@@ -728,8 +750,8 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const Blo
         s = fmaf(r, r, s);
         top = max(top, magnitude(weighted(r, k)));
     }
-    const float pre = rsqrtf(row_sum(s, part_pre, 0, warps, warp) / static_cast<float>(D) + a.eps);
-    const TokenGrid g = token_grid<false>(row_max(top, part_top, 0, warps, warp));
+    const float pre = rsqrtf(row_sum(s, part_pre, row) / static_cast<float>(D) + a.eps);
+    const TokenGrid g = token_grid<false>(row_max(top, part_top, row));
     int sum = 0;
     for (int k = threadIdx.x; k < D; k += kWideThreads) {
         const float r = value(k);
@@ -744,7 +766,7 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const Blo
     }
     if (!a.q) return;
     if (a.q_sums) {
-        sum = row_sum_first(sum, part_sum, 0, warps, warp);
+        sum = row_sum_first(sum, part_sum, row);
         if (threadIdx.x == 0) a.q_sums[m] = sum;
     }
     if (threadIdx.x == 0) a.q_scales[m] = g.scale * pre;
@@ -769,38 +791,55 @@ bool chunks_ok(const void* p, int64_t ld)
     return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * sizeof(T) % 16 == 0);
 }
 
-// Launches kernel(args, warps of a row): `cols` elements a row with what a
-// row off its boundaries needs in front, CH chunks a thread, at least four
-// warps a block.
-template <typename T, int CH, typename Args>
-int launch_rows(void (*kernel)(Args, int), const Args& args, int64_t M, int64_t cols, cudaStream_t stream)
+// Launches kernel(args, threads of a row): `chunks` 16-byte pieces a row, CH a
+// thread; blocks of 128 threads at least.
+template <int CH, bool SHORT, typename Args>
+int launch_rows(void (*kernel)(Args, int), const Args& args, int64_t M, int64_t chunks, cudaStream_t stream)
 {
-    const int warps = static_cast<int>((cols + 32 * kVec<T> * CH - 1) / (32 * kVec<T> * CH));
-    const int rows = std::max(1, 4 / warps);
-    kernel<<<static_cast<unsigned>((M + rows - 1) / rows), 32 * warps * rows, 0, stream>>>(args, warps);
+    const int threads = SHORT ? (chunks <= 8 ? 8 : 16) : static_cast<int>((chunks + 32 * CH - 1) / (32 * CH)) * 32;
+    const int rows = std::max(1, 128 / threads);
+    kernel<<<static_cast<unsigned>((M + rows - 1) / rows), threads * rows, 0, stream>>>(args, threads);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
 
 // Chunks a thread: one where there are few rows (the latency of a row counts)
 // or a row is one warp's anyway, else up to four, which keep more bytes on
-// their way a thread and need fewer warps to meet.
+// their way a thread and need fewer warps to meet (norm of 16384 x 4096: 91 us
+// with four, 119 with two, 167 with one).  0: one, and part of a warp a row
+// (norm of 500000 x 128: 91 us against 157 with a warp a row).
 template <typename T>
-int chunks_a_thread(int64_t M, int64_t cols)
+int chunks_a_thread(int64_t M, int64_t chunks)
 {
-    const int64_t chunks = (cols + kVec<T> - 1) / kVec<T>;
+    if (chunks <= 16) return 0;
     if (M <= 2 * sm_count() && chunks <= 1024) return 1;
     return chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
 }
 
+template <typename T, bool SHIFT>
+int64_t chunks_of(int64_t cols) { return (cols + (SHIFT ? kVec<T> - 1 : 0) + kVec<T> - 1) / kVec<T>; }
+
 template <typename T, bool SHIFT, bool GATE>
 int tokens_chunked(const TokenArgs& a, cudaStream_t stream)
 {
-    const int64_t cols = a.K + (SHIFT ? kVec<T> - 1 : 0);
-    switch (chunks_a_thread<T>(a.M, cols)) {
-        case 1: return launch_rows<T, 1>(quantize_tokens_kernel<T, 1, SHIFT, GATE>, a, a.M, cols, stream);
-        case 2: return launch_rows<T, 2>(quantize_tokens_kernel<T, 2, SHIFT, GATE>, a, a.M, cols, stream);
-        default: return launch_rows<T, 4>(quantize_tokens_kernel<T, 4, SHIFT, GATE>, a, a.M, cols, stream);
+    const int64_t chunks = chunks_of<T, SHIFT>(a.K);
+    switch (chunks_a_thread<T>(a.M, chunks)) {
+        case 0: return launch_rows<1, true>(quantize_tokens_kernel<T, 1, SHIFT, GATE, true>, a, a.M, chunks, stream);
+        case 1: return launch_rows<1, false>(quantize_tokens_kernel<T, 1, SHIFT, GATE, false>, a, a.M, chunks, stream);
+        case 2: return launch_rows<2, false>(quantize_tokens_kernel<T, 2, SHIFT, GATE, false>, a, a.M, chunks, stream);
+        default: return launch_rows<4, false>(quantize_tokens_kernel<T, 4, SHIFT, GATE, false>, a, a.M, chunks, stream);
+    }
+}
+
+template <typename T, bool SHIFT, bool GATE>
+int norm_chunked(const BlockNormArgs& a, cudaStream_t stream)
+{
+    const int64_t chunks = chunks_of<T, SHIFT>(a.D);
+    switch (chunks_a_thread<T>(a.M, chunks)) {
+        case 0: return launch_rows<1, true>(block_norm_kernel<T, 1, SHIFT, GATE, true>, a, a.M, chunks, stream);
+        case 1: return launch_rows<1, false>(block_norm_kernel<T, 1, SHIFT, GATE, false>, a, a.M, chunks, stream);
+        case 2: return launch_rows<2, false>(block_norm_kernel<T, 2, SHIFT, GATE, false>, a, a.M, chunks, stream);
+        default: return launch_rows<4, false>(block_norm_kernel<T, 4, SHIFT, GATE, false>, a, a.M, chunks, stream);
     }
 }
 
@@ -815,17 +854,6 @@ int tokens_typed(const TokenArgs& a, cudaStream_t stream)
     }
     if (whole) return a.gate ? tokens_chunked<T, false, true>(a, stream) : tokens_chunked<T, false, false>(a, stream);
     return a.gate ? tokens_chunked<T, true, true>(a, stream) : tokens_chunked<T, true, false>(a, stream);
-}
-
-template <typename T, bool SHIFT, bool GATE>
-int norm_chunked(const BlockNormArgs& a, cudaStream_t stream)
-{
-    const int64_t cols = a.D + (SHIFT ? kVec<T> - 1 : 0);
-    switch (chunks_a_thread<T>(a.M, cols)) {
-        case 1: return launch_rows<T, 1>(block_norm_kernel<T, 1, SHIFT, GATE>, a, a.M, cols, stream);
-        case 2: return launch_rows<T, 2>(block_norm_kernel<T, 2, SHIFT, GATE>, a, a.M, cols, stream);
-        default: return launch_rows<T, 4>(block_norm_kernel<T, 4, SHIFT, GATE>, a, a.M, cols, stream);
-    }
 }
 
 template <typename T>
