@@ -31,6 +31,12 @@
 //    of tensor memory, barriers and clusters costs more than the products.
 //    1 x 4096 x 4096 3.6 us (4.7 TB/s), 1 x 28672 x 8192 38.5 us (6.1 TB/s).
 //
+// All kernels are programmatic dependent launches: they may start while the
+// kernel before them ends, set themselves up, and wait for its results
+// (pdl_wait) before their first global access.  They let the next kernel start
+// once they hold their tensor memory, never before.  5 to 7% in a chain of such
+// kernels (a decoder layer's, 24 tokens: 63 us against 68).
+//
 // The two threads of a CTA that issue loads and MMAs are the elected ones of
 // their warps: under a plain lane test every such instruction took about 110
 // cycles to issue instead of 45, and with that the issue bound the kernels
@@ -260,6 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster::sync();   // both CTAs' barriers and tensor memory exist before any use
     tc_fence_after();
+    pdl_trigger();
+    pdl_wait();
     const uint32_t tbase = S.tmem_base;
     volatile int* abort = &S.abort;
 
@@ -416,6 +424,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         mbar_init(&S.done, 1);
         S.abort = 0;
         fence_mbar_init();
+        pdl_wait();
         // the first loads are on their way before the block has met
         for (int k = 0; k < first; ++k) load(k, k);
     }
@@ -426,6 +435,8 @@ __global__ void __launch_bounds__(kSplitThreads)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_trigger();
+    pdl_wait();
     const uint32_t tbase = S.tmem_base;
     volatile int* abort = &S.abort;
 
@@ -574,6 +585,8 @@ template <int MT, int U, int W, typename T>
 __global__ void __launch_bounds__(W * 32) w8a8_few_kernel(const W8A8Args a)
 {
     __shared__ int part[W][8 * MT][kFewRows];
+    pdl_trigger();
+    pdl_wait();
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -691,8 +704,9 @@ int launch_pair(const W8A8Args& a, cudaStream_t stream)
     if (rc) return rc;
     const int64_t n_tiles = (a.N + 2 * kRows - 1) / (2 * kRows), m_tiles = (a.M + NT - 1) / NT;
     const int pairs = static_cast<int>(std::min<int64_t>(n_tiles * m_tiles, sm_count() / 2));
-    w8a8_pair_kernel<NT, T><<<2 * pairs, kPairThreads, smem, stream>>>(
-        mapW, mapX, a, static_cast<int>(n_tiles), static_cast<int>(m_tiles), device_status_ptr());
+    const cudaError_t e = launch_k(w8a8_pair_kernel<NT, T>, dim3(2 * pairs), dim3(kPairThreads), smem, stream, true, mapW, mapX, a,
+                                   static_cast<int>(n_tiles), static_cast<int>(m_tiles), device_status_ptr());
+    if (e != cudaSuccess) return cuda_fail(e);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
@@ -721,13 +735,15 @@ int launch_split(const W8A8Args& a, int splits, cudaStream_t stream)
     cfg.blockDim = dim3(kSplitThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = splits;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, w8a8_split_kernel<NT, T>, mapW, mapX, a, splits, stages, device_status_ptr());
     if (e != cudaSuccess) return cuda_fail_msg("w8a8: cluster launch", e);
     GPTQ_LAUNCH_CHECK();
@@ -738,7 +754,10 @@ template <int MT, int U, int W, typename T>
 int launch_few(const W8A8Args& a, cudaStream_t stream)
 {
     const unsigned blocks = static_cast<unsigned>((a.N + kFewRows - 1) / kFewRows);
-    w8a8_few_kernel<MT, U, W, T><<<blocks, W * 32, 0, stream>>>(a);
+    // with many small blocks an early start puts more of them on the SMs that
+    // happen to finish first (1 x 11008 x 4096 9.7 us in a row against 9.2)
+    const cudaError_t e = launch_k(w8a8_few_kernel<MT, U, W, T>, dim3(blocks), dim3(W * 32), 0, stream, W == 8, a);
+    if (e != cudaSuccess) return cuda_fail(e);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
@@ -779,15 +798,18 @@ Choice choose_tiles(int64_t M, int64_t N, int64_t K)
     for (int nt : {32, 64, 128}) {
         if (nt > 32 && nt / 2 >= M) break;   // half the tile would be empty
         const int64_t tiles = (N + kRows - 1) / kRows * ((M + nt - 1) / nt);
-        // one CTA an SM while each keeps 4 stages of K, two while it keeps 8
-        const int64_t one = std::min<int64_t>(sm_count() / tiles, static_cast<int64_t>(blocks) / 4);
+        // one CTA an SM while each keeps 2 stages of K, two while it keeps 8;
+        // large clusters only where they are few (500 x 512 x 4096: 6.9 us by
+        // 4, 9.4 by 8: they do not spread over all SMs)
+        const int64_t one = std::min<int64_t>(sm_count() / tiles, static_cast<int64_t>(blocks) / 2);
         const int64_t two = std::min<int64_t>(2 * sm_count() / tiles, static_cast<int64_t>(blocks) / 8);
-        const int splits = static_cast<int>(std::min<int64_t>(kMaxSplits, std::max<int64_t>({1, one, two})));
+        const int64_t most = tiles <= 8 ? kMaxSplits : tiles <= 24 ? 6 : 4;
+        const int splits = static_cast<int>(std::min(most, std::max<int64_t>({1, one, two})));
         const double own = std::ceil(blocks / splits);
         const double rounds = std::ceil(static_cast<double>(tiles) * splits / (2 * sms));
         const double ends = 3.5 + 0.008 * nt + 0.03 * nt / splits + 0.012 * std::max(0.0, tiles * splits - sms);
-        consider({nt, splits}, static_cast<double>(tiles) * splits, ends, rounds * own * 0.2,
-                 static_cast<double>(tiles) * splits * own * (kRows + nt) * kBK);
+        const double ctas = static_cast<double>(tiles) * splits;
+        consider({nt, splits}, ctas, ends, rounds * own * 0.2, ctas * own * (kRows + nt) * kBK / std::min(1.0, ctas / sms / 1.5));
     }
     const struct { int nt; double ends, stage; } pairs[] = {{64, 4.9, 0.24}, {128, 5.6, 0.235}, {256, 7.5, 0.285}};
     for (const auto& p : pairs) {
