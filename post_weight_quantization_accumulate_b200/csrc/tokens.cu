@@ -37,7 +37,6 @@ namespace gptq {
 
 namespace {
 
-constexpr int kHeldCols = 16384;    // longest row kept in registers
 constexpr int kWideThreads = 1024;
 
 __device__ __forceinline__ float load_as_f32(const float* p) { return *p; }
@@ -102,6 +101,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 
+// The longest row kept in registers: four chunks a thread.
+template <typename T>
+constexpr int kHeldCols = 4 * kWideThreads * kVec<T>;
+
 // A row and a chunk of it: elements k .. k + kVec<T> - 1, of which those in
 // 0 .. K - 1 are there.  SHIFT: the row may begin off a 16-byte boundary (k
 // may then be negative, and the last chunk partial); else every chunk is whole.
@@ -139,14 +142,15 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rows pass the L1 cache by, so that the weights stay in it.  (Not the
-// read-only path: a row may be written in place.)  Weights are float32.
+// Rows pass the L1 cache by, so that what every row reads stays in it.  Not by
+// the read-only path: a row may be written in place, and a kernel that was
+// started early was there before its inputs were.
 template <typename T, bool KEEP>
 __device__ __forceinline__ uint4 load16(const T* p)
 {
     uint4 u;
     if constexpr (KEEP)
-        u = __ldg(reinterpret_cast<const uint4*>(p));
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
     else
         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
@@ -511,13 +515,8 @@ struct TokenArgs {
     int64_t ahead;
 };
 
-// Threads a row has at most; with 1024 / that many blocks an SM at least, a
-// thread has 64 registers.
-template <typename T, int CH>
-constexpr int max_row_threads() { return kHeldCols / (kVec<T> * CH) < 1024 ? kHeldCols / (kVec<T> * CH) : 1024; }
-
 template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT>
-__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) quantize_tokens_kernel(const TokenArgs a, int threads)
+__global__ void __launch_bounds__(kWideThreads) quantize_tokens_kernel(const TokenArgs a, int threads)
 {
     constexpr int VEC = kVec<T>;
     __shared__ uint32_t part_top[32];
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threa
 }
 
 template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT>
-__global__ void __launch_bounds__(max_row_threads<T, CH>(), 1024 / max_row_threads<T, CH>()) block_norm_kernel(const BlockNormArgs a, int threads)
+__global__ void __launch_bounds__(kWideThreads) block_norm_kernel(const BlockNormArgs a, int threads)
 {
     constexpr int VEC = kVec<T>;
     __shared__ float part_post[32], part_pre[32];
@@ -866,7 +865,7 @@ template <typename T>
 int tokens_typed(const TokenArgs& a, cudaStream_t stream)
 {
     const bool whole = a.K % kVec<T> == 0 && chunks_ok<T>(a.X, a.ldx) && chunks_ok<T>(a.gate, a.ldg) && chunks_ok<T>(a.hat, a.ldh);
-    if (a.K + (whole ? 0 : kVec<T> - 1) > kHeldCols) {
+    if (a.K + (whole ? 0 : kVec<T> - 1) > kHeldCols<T>) {
         const cudaError_t e = launch_k(quantize_wide_tokens_kernel<T>, dim3(static_cast<unsigned>(a.M)), dim3(kWideThreads), 0, stream, true, a);
         if (e != cudaSuccess) return cuda_fail(e);
         GPTQ_LAUNCH_CHECK();
@@ -882,7 +881,7 @@ int norm_typed(const BlockNormArgs& a, cudaStream_t stream)
     const bool whole = a.D % kVec<T> == 0 && chunks_ok<T>(a.block, a.ldb) && chunks_ok<T>(a.residual, a.ldr) &&
                        chunks_ok<T>(a.gate, a.ldg) && chunks_ok<T>(a.out, a.ldo) && chunks_ok<T>(a.stream_out, a.lds) &&
                        chunks_ok<float>(a.post_weight, 4) && chunks_ok<float>(a.pre_weight, 4);
-    if (a.D + (whole ? 0 : kVec<T> - 1) > kHeldCols) {
+    if (a.D + (whole ? 0 : kVec<T> - 1) > kHeldCols<T>) {
         const cudaError_t e = launch_k(block_norm_wide_kernel<T>, dim3(static_cast<unsigned>(a.M)), dim3(kWideThreads), 0, stream, true, a);
         if (e != cudaSuccess) return cuda_fail(e);
         GPTQ_LAUNCH_CHECK();

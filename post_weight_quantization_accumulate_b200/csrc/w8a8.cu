@@ -552,10 +552,18 @@ __global__ void __launch_bounds__(kSplitThreads)
 // in whole lines, U steps in flight a warp.
 constexpr int kFewRows = 16;
 
+// Not by the read-only path: the kernel may have started before its inputs
+// were there.
+__device__ __forceinline__ uint4 load_tokens(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ uint4 load_once(const void* p)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(W * 32) w8a8_few_kernel(const W8A8Args a)
                 w[u][h][1] = k < K ? load_once(w1 + k) : zero;
 #pragma unroll
                 for (int j = 0; j < MT; ++j)
-                    xb[u][h][j] = k < K ? first_codes(__ldg(reinterpret_cast<const uint4*>(x[j] + k)), K - k) : zero;
+                    xb[u][h][j] = k < K ? first_codes(load_tokens(x[j] + k), K - k) : zero;
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -797,6 +805,7 @@ Choice choose_tiles(int64_t M, int64_t N, int64_t K)
     };
     for (int nt : {32, 64, 128}) {
         if (nt > 32 && nt / 2 >= M) break;   // half the tile would be empty
+        if ((M + nt - 1) / nt > 65535) continue;   // the grid's second dimension
         const int64_t tiles = (N + kRows - 1) / kRows * ((M + nt - 1) / nt);
         // one CTA an SM while each keeps 2 stages of K, two while it keeps 8;
         // large clusters only where they are few (500 x 512 x 4096: 6.9 us by
