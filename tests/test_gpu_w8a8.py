@@ -79,7 +79,7 @@ def _tokens(x, gate=None, pitch=None):
 
 
 TOKEN_SIZES = [(1, 1), (1, 4096), (3, 2), (5, 7), (2, 64), (17, 1000), (33, 1003), (300, 4096), (7, 11008), (2, 28672),
-               (3, 65536), (2, 65535), (1000, 40)]
+               (3, 65536), (2, 65535), (1000, 40), (300, 61), (77, 125), (33, 128), (515, 16), (2, 32761), (2, 32768)]
 
 
 @pytest.mark.parametrize("M,K", TOKEN_SIZES)
@@ -264,7 +264,7 @@ def _check_norm(M, D, t, post_norm=True, weights=True, gate_rows=1, scale=0.5, e
 
 
 @pytest.mark.parametrize("M,D", [(1, 1), (1, 4096), (2, 3), (5, 64), (33, 1000), (3, 1003), (300, 4096), (19, 5003), (4, 11008),
-                                 (2, 28672), (2, 65536), (2, 65535), (513, 72)])
+                                 (2, 28672), (2, 65536), (2, 65535), (513, 72), (300, 61), (33, 128), (2, 32761)])
 @pytest.mark.parametrize("t", [BF16, F16, F32])
 def test_norm_sizes_and_types(M, D, t):
     _check_norm(M, D, t)
@@ -355,7 +355,8 @@ def _check_product(M, N, K, t, zeros=True, bias=True, extreme=False, pitch_x=Non
 PRODUCT_SIZES = [(1, 1, 1), (1, 128, 4096), (1, 4096, 4096), (2, 77, 1003), (3, 130, 16), (4, 64, 11008), (5, 200, 96), (8, 384, 640),
                  (9, 1000, 4096), (16, 256, 768), (17, 129, 513), (31, 4096, 100), (33, 257, 2048), (64, 512, 1024),
                  (70, 260, 640), (128, 128, 4096), (129, 300, 300), (200, 1030, 1500), (256, 256, 256), (257, 511, 129),
-                 (400, 4096, 256), (1000, 1003, 515), (2048, 2048, 512), (3000, 40, 1000)]
+                 (400, 4096, 256), (1000, 1003, 515), (2048, 2048, 512), (3000, 40, 1000), (200, 300, 1), (40, 130, 5), (500, 512, 2048),
+                 (12, 5000, 7000), (6, 7200, 200), (700, 5000, 300)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCT_SIZES)
@@ -515,6 +516,91 @@ def test_streams_and_graphs():
     want = step()
     _done()
     assert all(torch.equal(u, v) for u, v in zip(want, kept))
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose elements lie more than 2^31 elements into their tensors."""
+    x = torch.empty(40000, 65536, dtype=BF16, device="cuda")[:, :200]        # 5 GB, pitch 65536
+    x.normal_(generator=torch.Generator("cuda").manual_seed(1))
+    t = w8a8.quantize_tokens(x)
+    out = torch.empty(40000, 65536, dtype=BF16, device="cuda")[:, :200]
+    B.gptq_block_norm(None, x, out=out)
+    _done()
+    for at in (slice(0, 50), slice(39950, 40000)):
+        want = w8a8.quantize_tokens(x[at].contiguous())
+        assert torch.equal(t.codes[at], want.codes) and torch.equal(t.sums[at], want.sums)
+        assert torch.equal(out[at], w8a8.block_norm(None, x[at].contiguous())[1])
+    del x, out
+    M = N = 47000                                                           # Y of 2.2e9 elements
+    _, xd = _codes(1, M, 48)
+    _, wd = _codes(2, N, 48)
+    ones = torch.ones(M, device="cuda")
+    y = w8a8.linear(w8a8.Tokens(xd, ones), w8a8.Weight(wd, ones))
+    _done()
+    assert torch.equal(y[-3:].float(), (xd[-3:].float() @ wd.float().t()).to(BF16).float())
+    assert torch.equal(y[:, -3:].float(), (xd.float() @ wd[-3:].float().t()).to(BF16).float())
+
+
+@pytest.mark.parametrize("M", [1, 20, 90, 300, 1500])
+def test_calls_in_a_row_without_waiting(M):
+    """The kernels start before the one before them ends: a chain in which each
+    call reads what the last one wrote, over the same buffers, against the
+    same calls with a wait after each."""
+    D, N = 512, 520
+    _, w1 = _codes(3, N, D)
+    _, w2 = _codes(4, D, N)
+    u = torch.rand(N, device="cuda") * 1e-3 + 1e-4
+    a, b = w8a8.Weight(w1, u), w8a8.Weight(w2, u[:D].contiguous(), torch.randint(-9, 9, (D,), device="cuda", dtype=torch.int32))
+    x0 = _randn(M, M, D).to(BF16).cuda()
+
+    def chain(wait):
+        rest = (lambda: torch.cuda.synchronize()) if wait else (lambda: None)
+        x, h = x0.clone(), torch.zeros(M, D, dtype=BF16, device="cuda")
+        y = torch.empty(M, N, dtype=BF16, device="cuda")
+        q, s, n = w8a8.empty_codes(M, D, "cuda"), torch.empty(M, device="cuda"), torch.empty(M, dtype=torch.int32, device="cuda")
+        q2 = w8a8.empty_codes(M, N, "cuda")
+        rest()
+        for _ in range(12):
+            B.gptq_block_norm(h, x, stream_out=x, q=q, q_scales=s, q_sums=n, scale=0.5)
+            rest()
+            B.gptq_w8a8_gemm(y, q, s, a.codes, a.scales)
+            rest()
+            B.gptq_quantize_tokens(q2, s, n, y, y)
+            rest()
+            B.gptq_w8a8_gemm(h, q2, s, b.codes, b.scales, n, b.zeros)
+            rest()
+        torch.cuda.synchronize()
+        return x, h, y, q, q2
+
+    want = chain(True)
+    for _ in range(3):
+        got = chain(False)
+        assert all(torch.equal(u, v) for u, v in zip(want, got))
+    _done()
+
+
+def test_products_on_two_streams_at_once():
+    """Kernels that hold tensor memory, on two streams, in every size class."""
+    sizes = [(20, 700, 1024), (64, 4096, 2048), (300, 600, 512), (1000, 1000, 700), (1, 4096, 512)]
+    jobs = []
+    for M, N, K in sizes:
+        _, xd = _codes(M, M, K)
+        _, wd = _codes(N, N, K)
+        jobs.append((w8a8.Tokens(xd, torch.rand(M, device="cuda")), w8a8.Weight(wd, torch.rand(N, device="cuda"))))
+    want = [w8a8.linear(t, w) for t, w in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for r in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append([w8a8.linear(t, w) for t, w in (jobs if i else jobs[::-1])])
+    for s in streams:
+        s.synchronize()
+    _done()
+    for k, g in enumerate(got):
+        for y, v in zip(want, g if k % 2 else g[::-1]):
+            assert torch.equal(y, v)
 
 
 def test_decoder_layer_in_8_bits():
