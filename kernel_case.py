@@ -5,6 +5,8 @@
     python kernel_case.py \
         --call w4a16 [--m M] [--n N] [--k K] [--group-size G] [--path 0|1|2] [--reps R]
     python kernel_case.py \
+        --call w8a8|tokens|block_norm [--m M] [--n N] [--k K] [--gated] [--reps R]
+    python kernel_case.py \
         --call hessian_f32 --workload q_proj_4096 --tokens N [--reps R]
 
 The inputs follow the workload's recipe (see synth.py) with `--tokens`
@@ -25,7 +27,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
 from post_weight_quantization_accumulate_b200 import binding as B  # noqa: E402
-from post_weight_quantization_accumulate_b200 import synth  # noqa: E402
+from post_weight_quantization_accumulate_b200 import synth, w8a8  # noqa: E402
 from post_weight_quantization_accumulate_b200.layer import LayerQuantizer  # noqa: E402
 
 
@@ -84,6 +86,45 @@ def w4a16_case(a):
           f"{min(ms[1:]) * 1e3:.1f} us/call (cold L2, single launch), status {B.gptq_device_status()}")
 
 
+def w8a8_case(a):
+    """The 8-bit calls on seeded operands: the product of m tokens with an n x
+    k weight, the tokens of m x k values (`--gated`: of a gated activation),
+    and the norm between two blocks of m x k (`--gated`: with norm and gate
+    after the block); a 256 MB buffer is rewritten before every call."""
+    dev = torch.device("cuda", 0)
+    g = torch.Generator(dev).manual_seed(7)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device=dev)
+
+    x, y = normal(a.m, a.k).to(torch.bfloat16), normal(a.m, a.k).to(torch.bfloat16)
+    if a.call == "w8a8":
+        t = w8a8.quantize_tokens(x)
+        codes = w8a8.empty_codes(a.n, a.k, dev)
+        codes.copy_((normal(a.n, a.k) * 40).round().clamp(-127, 127))
+        w = w8a8.Weight(codes, torch.rand(a.n, generator=g, device=dev),
+                        torch.randint(-20, 21, (a.n,), generator=g, device=dev, dtype=torch.int32))
+        call = lambda: w8a8.linear(t, w)  # noqa: E731
+    elif a.call == "tokens":
+        call = lambda: w8a8.quantize_tokens(x, gate=y if a.gated else None)  # noqa: E731
+    else:
+        pre = 1 + 0.1 * normal(a.k)
+        kw = {"post_norm": True, "post_weight": pre, "gate": y[:1], "gate_rows": a.m} if a.gated else {}
+        call = lambda: w8a8.block_norm(x, y, pre, **kw)  # noqa: E731
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=dev)
+    ms = []
+    for _ in range(a.reps + 1):
+        flush.fill_(1)
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        call()
+        e1.record()
+        torch.cuda.synchronize()
+        ms.append(e0.elapsed_time(e1))
+    print(f"{a.call} m={a.m} n={a.n} k={a.k} gated={a.gated}: {min(ms[1:]) * 1e3:.1f} us/call (cold L2, single launch), "
+          f"status {B.gptq_device_status()}")
+
+
 def hessian_f32_case(a):
     """gptq_hessian_accumulate_f32 on the workload's fp32 activation draw
     (`--tokens` of them), 8192-token chunks."""
@@ -112,7 +153,7 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--call", default="hessian",
                     choices=["hessian", "hessian_f32", "prepare", "quantize", "quantize_q4k", "layer",
-                             "tf32_peak", "w4a16"])
+                             "tf32_peak", "w4a16", "w8a8", "tokens", "block_norm"])
     ap.add_argument("--workload", default="q_proj_4096")
     ap.add_argument("--tokens", type=int, default=None)
     ap.add_argument("--reps", type=int, default=3)
@@ -121,12 +162,16 @@ def main():
     ap.add_argument("--k", type=int, default=4096)
     ap.add_argument("--group-size", type=int, default=128)
     ap.add_argument("--path", type=int, default=0)
+    ap.add_argument("--gated", action="store_true")
     a = ap.parse_args()
     if a.call == "tf32_peak":
         tf32_peak()
         return
     if a.call == "w4a16":
         w4a16_case(a)
+        return
+    if a.call in ("w8a8", "tokens", "block_norm"):
+        w8a8_case(a)
         return
     if a.call == "hessian_f32":
         hessian_f32_case(a)

@@ -142,19 +142,30 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int o)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rows pass the L1 cache by, so that what every row reads stays in it.  Not by
-// the read-only path: a row may be written in place, and a kernel that was
-// started early was there before its inputs were.
-template <typename T, bool KEEP>
-__device__ __forceinline__ uint4 load16(const T* p)
+// 16 bytes, or four times `other` where they are not there (a predicate, no
+// branch: with 8 values a chunk, the branches around its loads and stores were
+// a sixth of the instructions).  Rows pass the L1 cache by, so that what every
+// row reads (KEEP) stays in it.  Not by the read-only path: a row may be
+// written in place, and a kernel that was started early was there before its
+// inputs were.
+template <bool KEEP>
+__device__ __forceinline__ uint4 load16(const void* p, bool there, uint32_t other = 0u)
 {
     uint4 u;
     if constexpr (KEEP)
-        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "mov.b32 %0, %6;\n\tmov.b32 %1, %6;\n\tmov.b32 %2, %6;\n\tmov.b32 %3, %6;\n\t"
+            "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+            : "=&r"(u.x), "=&r"(u.y), "=&r"(u.z), "=&r"(u.w)
+            : "l"(p), "r"(static_cast<uint32_t>(there)), "r"(other));
     else
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "l"(p));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "mov.b32 %0, %6;\n\tmov.b32 %1, %6;\n\tmov.b32 %2, %6;\n\tmov.b32 %3, %6;\n\t"
+            "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+            : "=&r"(u.x), "=&r"(u.y), "=&r"(u.z), "=&r"(u.w)
+            : "l"(p), "r"(static_cast<uint32_t>(there)), "r"(other));
     return u;
 }
 
@@ -162,17 +173,16 @@ __device__ __forceinline__ uint4 load16(const T* p)
 // of another 16 is touched.
 __device__ __forceinline__ uint4 piece(uintptr_t p, uintptr_t lo, uintptr_t hi)
 {
-    return p + 16 > lo && p < hi ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+    return load16<true>(reinterpret_cast<const void*>(p), p + 16 > lo && p < hi);
 }
 
 template <typename T, bool SHIFT, bool KEEP = false>
 __device__ __forceinline__ uint4 load_chunk(const T* row, int k, int K, bool live)
 {
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (!SHIFT) {
-        return live && k < K ? load16<T, KEEP>(row + k) : zero;
+        return load16<KEEP>(row + k, live && k < K);
     } else {
-        if (!live || k >= K) return zero;
+        if (!live || k >= K) return make_uint4(0u, 0u, 0u, 0u);
         const uintptr_t lo = reinterpret_cast<uintptr_t>(row), hi = lo + K * sizeof(T);
         const uintptr_t at = lo + static_cast<int64_t>(k) * static_cast<int64_t>(sizeof(T));
         const int o = static_cast<int>(at & 15);
@@ -223,13 +233,19 @@ __device__ __forceinline__ void store_chunk(T* row, int k, int K, const Chunk<T>
     }
 }
 
-// c *= the float32 weights of the chunk's elements.
+// c *= the float32 weights of the chunk's elements, where there are any.
 template <typename T, bool SHIFT>
-__device__ __forceinline__ void times_weights(Chunk<T>& c, const float* w, int k, int K)
+__device__ __forceinline__ void times_weights(Chunk<T>& c, const float* w, int k, int K, bool any)
 {
+    if (SHIFT && (!any || k >= K)) return;
 #pragma unroll
     for (int i = 0; i < kVec<T> / 4; ++i) {
-        const Chunk<float> f = widen_chunk<float>(load_chunk<float, SHIFT, true>(w, k + 4 * i, K, true));
+        uint4 u;
+        if constexpr (SHIFT)
+            u = load_chunk<float, true, true>(w, k + 4 * i, K, true);
+        else
+            u = load16<true>(w + k + 4 * i, any && k < K, 0x3f800000u);
+        const Chunk<float> f = widen_chunk<float>(u);
         c.v[2 * i] = mul2(c.v[2 * i], f.v[0]);
         c.v[2 * i + 1] = mul2(c.v[2 * i + 1], f.v[1]);
     }
@@ -361,6 +377,8 @@ constexpr float kRound = 12582912.f;
 enum CodeKind { kZeros, kMultiply, kDivide };
 
 struct TokenGrid {
+    __device__ bool plain() const { return kind == kMultiply && c == 1.f; }
+
     CodeKind kind;   // kZeros: a row of zeros, or one that holds an infinity or NaN
     float scale;     // t / 127; NaN for a row that is not finite
     float c, t, r;   // 2^0 or 2^+-100; c times the maximum; 127 / t rounded up
@@ -425,16 +443,13 @@ __device__ __forceinline__ float2 code_pair(float2 v, const TokenGrid& g)
     return make_float2(code(v.x), code(v.y));
 }
 
-template <typename T, bool ELEVEN, bool EXACT>
+// A chunk's; PLAIN: a row of kind kMultiply with c = 1.
+template <typename T, bool ELEVEN, bool EXACT, bool PLAIN>
 __device__ __forceinline__ void code_chunk(Chunk<T>& c, const TokenGrid& g)
 {
-    if (g.kind == kMultiply && g.c == 1.f) {
 #pragma unroll
-        for (int j = 0; j < kVec<T> / 2; ++j) c.v[j] = multiplied<EXACT>(c.v[j], g);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kVec<T> / 2; ++j) c.v[j] = code_pair<ELEVEN, EXACT>(c.v[j], g);
-    }
+    for (int j = 0; j < kVec<T> / 2; ++j)
+        c.v[j] = PLAIN ? multiplied<EXACT>(c.v[j], g) : code_pair<ELEVEN, EXACT>(c.v[j], g);
 }
 
 __device__ __forceinline__ uint32_t pack4(float2 a, float2 b)
@@ -459,6 +474,15 @@ __device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live,
         w[j] = pack4(c.v[2 * j], c.v[2 * j + 1]);
         sum = __dp4a(static_cast<int>(w[j]), 0x01010101, sum);
     }
+    if constexpr (!SHIFT) {
+        if (row && live && k < K) {
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint2*>(row + k) = make_uint2(w[0], w[VEC / 4 - 1]);
+            else
+                *reinterpret_cast<uint32_t*>(row + k) = w[0];
+        }
+        return sum;
+    }
     if (!row) return sum;
     const uint64_t own = VEC == 8 ? static_cast<uint64_t>(w[VEC / 4 - 1]) << 32 | w[0] : w[0];
     auto put = [&](uint64_t codes, int at, int from, int to) {   // codes[from .. to) at row[at + from ..)
@@ -472,17 +496,13 @@ __device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live,
                 if (at + j >= 0 && at + j < K) row[at + j] = static_cast<int8_t>(codes >> (8 * j));
         }
     };
-    if constexpr (!SHIFT) {
-        if (live && k < K) put(own, k, 0, VEC);
-    } else {
-        const int lead = (VEC - k % VEC) % VEC;   // codes that belong to the word before; the same for a whole row
-        uint64_t next = 0;
-        if (lead) next = __shfl_down_sync(0xffffffffu, own, 1);
-        if (live && k < K) {
-            if (lead && r.lane() == 0) put(own << (8 * (VEC - lead)), k + lead - VEC, VEC - lead, VEC);
-            const uint64_t word = lead ? own >> (8 * lead) | next << (8 * (VEC - lead)) : own;
-            put(word, k + lead, 0, lead && r.lane() == r.width() - 1 ? VEC - lead : VEC);
-        }
+    const int lead = (VEC - k % VEC) % VEC;   // codes that belong to the word before; the same for a whole row
+    uint64_t next = 0;
+    if (lead) next = __shfl_down_sync(0xffffffffu, own, 1);
+    if (live && k < K) {
+        if (lead && r.lane() == 0) put(own << (8 * (VEC - lead)), k + lead - VEC, VEC - lead, VEC);
+        const uint64_t word = lead ? own >> (8 * lead) | next << (8 * (VEC - lead)) : own;
+        put(word, k + lead, 0, lead && r.lane() == r.width() - 1 ? VEC - lead : VEC);
     }
     return sum;
 }
@@ -569,19 +589,27 @@ __global__ void __launch_bounds__(kWideThreads) quantize_tokens_kernel(const Tok
     constexpr bool ELEVEN = PACKED && std::is_same<T, __half>::value;
     const TokenGrid g = token_grid<ELEVEN>(row_max(top, part_top, row));
     int sum = 0;
+    int8_t* q = a.Xq ? a.Xq + m * a.ldq : nullptr;
+    auto finish = [&](auto plain) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int k = k0 + i * threads * VEC;
-        Chunk<T>& w = v[PACKED ? 0 : i];
-        if constexpr (PACKED) w = widen_chunk<T>(xr[i]);
-        code_chunk<T, ELEVEN, !GATE && sizeof(T) == 4>(w, g);
-        sum += store_codes<T, SHIFT>(a.Xq ? a.Xq + m * a.ldq : nullptr, k, a.K, live, w, row);
-        if (a.hat && live && k < a.K) {
+        for (int i = 0; i < CH; ++i) {
+            const int k = k0 + i * threads * VEC;
+            Chunk<T>& w = v[PACKED ? 0 : i];
+            if constexpr (PACKED) w = widen_chunk<T>(xr[i]);
+            code_chunk<T, ELEVEN, !GATE && sizeof(T) == 4, decltype(plain)::value>(w, g);
+            sum += store_codes<T, SHIFT>(q, k, a.K, live, w, row);
+            if (a.hat && live && k < a.K) {
 #pragma unroll
-            for (int j = 0; j < VEC / 2; ++j) w.v[j] = mul2(add2(w.v[j], both(-kRound)), both(g.scale));
-            store_chunk<T, SHIFT>(hat, k, a.K, w);
+                for (int j = 0; j < VEC / 2; ++j) w.v[j] = mul2(add2(w.v[j], both(-kRound)), both(g.scale));
+                store_chunk<T, SHIFT>(hat, k, a.K, w);
+            }
         }
-    }
+    };
+    // SHORT: the rows of a warp go the same way, for its lanes store together
+    if (SHORT ? __all_sync(0xffffffffu, g.plain()) : g.plain())
+        finish(std::true_type());
+    else
+        finish(std::false_type());
     if (a.x_sums) {
         sum = row_sum_first(sum, part_sum, row);
         if (live && tid == 0) a.x_sums[m] = sum;
@@ -633,6 +661,7 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_kernel(const BlockNor
         }
         scale *= rsqrtf(row_sum(s.x + s.y, part_post, row) / static_cast<float>(D) + a.eps);
     }
+    const bool weighted = a.post_norm && a.post_weight, store_stream = a.stream_out && live;
     Chunk<T> h[CH];
     float2 s = both(0.f);
     uint32_t top = 0;
@@ -640,7 +669,7 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_kernel(const BlockNor
     for (int i = 0; i < CH; ++i) {
         const int k = k0 + i * step;
         h[i] = widen_chunk<T>(br[i]);
-        if (a.post_norm && a.post_weight && k < D) times_weights<T, SHIFT>(h[i], a.post_weight, k, D);
+        times_weights<T, SHIFT>(h[i], a.post_weight, k, D, weighted);
         if (GATE) {
             const Chunk<T> f = widen_chunk<T>(gr[i]);
 #pragma unroll
@@ -652,10 +681,8 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_kernel(const BlockNor
             h[i].v[j] = fma2(both(scale), h[i].v[j], r.v[j]);
             s = fma2(h[i].v[j], h[i].v[j], s);
         }
-        if (live && k < D) {
-            if (a.stream_out) store_chunk<T, SHIFT>(stream_out, k, D, h[i]);
-            if (a.pre_weight) times_weights<T, SHIFT>(h[i], a.pre_weight, k, D);
-        }
+        if (store_stream && k < D) store_chunk<T, SHIFT>(stream_out, k, D, h[i]);
+        times_weights<T, SHIFT>(h[i], a.pre_weight, k, D, a.pre_weight);
         if (a.q) {
 #pragma unroll
             for (int j = 0; j < VEC / 2; ++j) top = max(max(top, magnitude(h[i].v[j].x)), magnitude(h[i].v[j].y));
@@ -677,11 +704,17 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_kernel(const BlockNor
     // the codes are those of r' w: the factor rsqrt(...) of the row cancels in 127 v / t
     const TokenGrid g = token_grid<false>(row_max(top, part_top, row));
     int sum = 0;
+    auto finish = [&](auto plain) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        code_chunk<T, false, false>(h[i], g);
-        sum += store_codes<T, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i], row);
-    }
+        for (int i = 0; i < CH; ++i) {
+            code_chunk<T, false, false, decltype(plain)::value>(h[i], g);
+            sum += store_codes<T, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i], row);
+        }
+    };
+    if (SHORT ? __all_sync(0xffffffffu, g.plain()) : g.plain())
+        finish(std::true_type());
+    else
+        finish(std::false_type());
     if (a.q_sums) {
         sum = row_sum_first(sum, part_sum, row);
         if (live && tid == 0) a.q_sums[m] = sum;
