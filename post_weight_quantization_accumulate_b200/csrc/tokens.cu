@@ -21,11 +21,11 @@
 // The kernels are programmatic dependent launches: set up while the kernel
 // before ends, waiting for its results before the first global access.
 //
-// B200: tokens of 8192 x 11008 bf16 with values 68 us (6.6 TB/s), without 54
-// (5.0), of a gated activation 98 (4.6, bound by instructions: 22 a value);
-// norm of 16384 x 4096 bf16 85 us (6.3 TB/s), with norm and gate after the block
-// 92 (5.8), to tokens 76 (6.2); 16384 x 5003 f16 (rows off their boundaries) 160
-// (4.1); one row of 4096 2.0 and 3.0.
+// B200: tokens of 8192 x 11008 bf16 with values 67 us (6.7 TB/s), without 48
+// (5.6), of a gated activation 77 (5.9; 20 instructions a value); norm of 16384 x
+// 4096 bf16 84 us (6.4 TB/s), with norm and gate after the block 89 (6.0), to
+// tokens 76 (6.2); 16384 x 5003 f16 (rows off their boundaries: shifts) 165 (4.0);
+// one row of 4096 1.9 and 2.9.
 #include "common.cuh"
 
 #include <cuda_bf16.h>
@@ -535,8 +535,8 @@ struct TokenArgs {
     int64_t ahead;
 };
 
-template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT>
-__global__ void __launch_bounds__(kWideThreads) quantize_tokens_kernel(const TokenArgs a, int threads)
+template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT, bool THREE = false>
+__global__ void __launch_bounds__(THREE ? 384 : kWideThreads, THREE ? 3 : 1) quantize_tokens_kernel(const TokenArgs a, int threads)
 {
     constexpr int VEC = kVec<T>;
     __shared__ uint32_t part_top[32];
@@ -617,8 +617,8 @@ __global__ void __launch_bounds__(kWideThreads) quantize_tokens_kernel(const Tok
     if (live && tid == 0) a.x_scales[m] = g.scale;
 }
 
-template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT>
-__global__ void __launch_bounds__(kWideThreads) block_norm_kernel(const BlockNormArgs a, int threads)
+template <typename T, int CH, bool SHIFT, bool GATE, bool SHORT, bool THREE = false>
+__global__ void __launch_bounds__(THREE ? 384 : kWideThreads, THREE ? 3 : 1) block_norm_kernel(const BlockNormArgs a, int threads)
 {
     constexpr int VEC = kVec<T>;
     __shared__ float part_post[32], part_pre[32];
@@ -870,6 +870,13 @@ int chunks_a_thread(int64_t M, int64_t chunks)
 template <typename T, bool SHIFT>
 int64_t chunks_of(int64_t cols) { return (cols + (SHIFT ? kVec<T> - 1 : 0) + kVec<T> - 1) / kVec<T>; }
 
+// Rows of 352 or 384 threads with four chunks each: at 64 registers a thread an
+// SM holds two of them, at 56 three (tokens of a gated activation of 8192 x
+// 11008: 77 us against 96; norm of 4096 x 11008 to tokens 57 against 66).  Not
+// for the norm with a gate or off its boundaries, which keep a third row's
+// chunks or shifts and would spill (96 against 88, 119 against 116).
+bool three_blocks(int64_t chunks) { return chunks > 4 * 320 && chunks <= 4 * 384; }
+
 template <typename T, bool SHIFT, bool GATE>
 int tokens_chunked(const TokenArgs& a, cudaStream_t stream)
 {
@@ -878,8 +885,11 @@ int tokens_chunked(const TokenArgs& a, cudaStream_t stream)
         case 0: return launch_rows<1, true>(quantize_tokens_kernel<T, 1, SHIFT, GATE, true>, a, a.M, chunks, stream);
         case 1: return launch_rows<1, false>(quantize_tokens_kernel<T, 1, SHIFT, GATE, false>, a, a.M, chunks, stream);
         case 2: return launch_rows<2, false>(quantize_tokens_kernel<T, 2, SHIFT, GATE, false>, a, a.M, chunks, stream);
-        default: return launch_rows<4, false>(quantize_tokens_kernel<T, 4, SHIFT, GATE, false>, a, a.M, chunks, stream);
+        default: break;
     }
+    if (three_blocks(chunks))
+        return launch_rows<4, false>(quantize_tokens_kernel<T, 4, SHIFT, GATE, false, true>, a, a.M, chunks, stream);
+    return launch_rows<4, false>(quantize_tokens_kernel<T, 4, SHIFT, GATE, false>, a, a.M, chunks, stream);
 }
 
 template <typename T, bool SHIFT, bool GATE>
@@ -890,8 +900,12 @@ int norm_chunked(const BlockNormArgs& a, cudaStream_t stream)
         case 0: return launch_rows<1, true>(block_norm_kernel<T, 1, SHIFT, GATE, true>, a, a.M, chunks, stream);
         case 1: return launch_rows<1, false>(block_norm_kernel<T, 1, SHIFT, GATE, false>, a, a.M, chunks, stream);
         case 2: return launch_rows<2, false>(block_norm_kernel<T, 2, SHIFT, GATE, false>, a, a.M, chunks, stream);
-        default: return launch_rows<4, false>(block_norm_kernel<T, 4, SHIFT, GATE, false>, a, a.M, chunks, stream);
+        default: break;
     }
+    if constexpr (!SHIFT && !GATE)
+        if (three_blocks(chunks))
+            return launch_rows<4, false>(block_norm_kernel<T, 4, SHIFT, GATE, false, true>, a, a.M, chunks, stream);
+    return launch_rows<4, false>(block_norm_kernel<T, 4, SHIFT, GATE, false>, a, a.M, chunks, stream);
 }
 
 template <typename T>
