@@ -438,7 +438,8 @@ int gptq_quantize_tokens(int8_t *Xq, int64_t ldq, float *x_scales, int32_t *x_su
  *     out = r' * rsqrt(mean_k r'^2 + eps) * pre_weight
  * in float32 from the inputs to the outputs: r' is rounded where it is
  * stored, not before the second norm.  Means of squares are sums in float32
- * (they overflow for rows of magnitude above about 1e19 / sqrt(D)).
+ * (they overflow for rows of magnitude above about 1e19 / sqrt(D), and with
+ * eps = 0 rows below 1e-19 have none).
  *   stream_out  r' [M, D] OUT or NULL; may be residual itself (lds = ldr).
  *   out         [M, D] OUT or NULL; may be block itself (ldo = ldb).
  *   q           int8 [M, D] OUT or NULL: out as 8-bit tokens, quantized from

@@ -821,15 +821,32 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const Blo
     if (threadIdx.x == 0) a.q_scales[m] = g.scale * pre;
 }
 
-__global__ void w8a8_pack_kernel(int8_t* Wq, int64_t ldw, int32_t* w_zeros, const uint8_t* codes,
-                                 const float* zeros, int64_t N, int64_t K)
+// -- the product's weights: 16 codes a thread, one pass at memory's rate (once
+// a layer)
+
+template <bool WHOLE>
+__global__ void w8a8_pack_kernel(int8_t* Wq, int64_t ldw, int32_t* w_zeros, const uint8_t* codes, const float* zeros, int64_t N,
+                                 int64_t K)
 {
-    const int64_t n = blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z;
-    if (n >= N) return;
-    for (int64_t k = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; k < ldw;
-         k += static_cast<int64_t>(gridDim.x) * blockDim.x)
-        Wq[n * ldw + k] = k < K ? static_cast<int8_t>(codes[n * K + k] ^ 0x80) : int8_t(0);
-    if (blockIdx.x == 0 && threadIdx.x == 0) w_zeros[n] = static_cast<int32_t>(zeros[n]) - 128;
+    const int64_t pieces = ldw / 16;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < N) w_zeros[i] = static_cast<int32_t>(zeros[i]) - 128;
+    for (int64_t p = i; p < N * pieces; p += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t n = p / pieces, k = 16 * (p % pieces);
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (WHOLE) {   // rows of whole, aligned pieces
+            if (k < K) {
+                u = *reinterpret_cast<const uint4*>(codes + n * K + k);
+                u = make_uint4(u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u);
+            }
+        } else {
+            uint8_t c[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) c[j] = k + j < K ? codes[n * K + k + j] ^ 0x80 : 0;
+            memcpy(&u, c, 16);
+        }
+        *reinterpret_cast<uint4*>(Wq + n * ldw + k) = u;
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -962,10 +979,13 @@ int run_block_norm(const BlockNormArgs& a0, int type, cudaStream_t stream)
 int run_w8a8_pack(int8_t* Wq, int64_t ldw, int32_t* w_zeros, const uint8_t* codes, const float* zeros,
                   int64_t N, int64_t K, cudaStream_t stream)
 {
-    const unsigned y = static_cast<unsigned>(std::min<int64_t>(N, 32768));
-    const unsigned z = static_cast<unsigned>((N + y - 1) / y);
-    w8a8_pack_kernel<<<dim3(static_cast<unsigned>(std::min<int64_t>((ldw + 255) / 256, 64)), y, z), 256, 0, stream>>>(
-        Wq, ldw, w_zeros, codes, zeros, N, K);
+    // every zero has a thread of its own; the pieces go round
+    const int64_t want = std::max(N, std::min(N * (ldw / 16), int64_t(sm_count()) * 2048 * 4));
+    const unsigned blocks = static_cast<unsigned>((want + 255) / 256);
+    if (K % 16 == 0 && reinterpret_cast<uintptr_t>(codes) % 16 == 0)
+        w8a8_pack_kernel<true><<<blocks, 256, 0, stream>>>(Wq, ldw, w_zeros, codes, zeros, N, K);
+    else
+        w8a8_pack_kernel<false><<<blocks, 256, 0, stream>>>(Wq, ldw, w_zeros, codes, zeros, N, K);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
 }
