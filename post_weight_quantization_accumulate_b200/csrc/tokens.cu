@@ -233,21 +233,49 @@ __device__ __forceinline__ void store_chunk(T* row, int k, int K, const Chunk<T>
     }
 }
 
-// c *= the float32 weights of the chunk's elements, where there are any.
+// c *= the float32 weights of the chunk's elements, where there are any.  Off
+// the boundaries: the aligned pieces that hold them, moved by whole words (the
+// same for all of a row), and 0 for elements that are not there, so that
+// nothing of what lies behind the weights meets the row's zeros.
 template <typename T, bool SHIFT>
 __device__ __forceinline__ void times_weights(Chunk<T>& c, const float* w, int k, int K, bool any)
 {
-    if (SHIFT && (!any || k >= K)) return;
+    constexpr int VEC = kVec<T>;
+    if constexpr (!SHIFT) {
 #pragma unroll
-    for (int i = 0; i < kVec<T> / 4; ++i) {
-        uint4 u;
-        if constexpr (SHIFT)
-            u = load_chunk<float, true, true>(w, k + 4 * i, K, true);
-        else
-            u = load16<true>(w + k + 4 * i, any && k < K, 0x3f800000u);
-        const Chunk<float> f = widen_chunk<float>(u);
-        c.v[2 * i] = mul2(c.v[2 * i], f.v[0]);
-        c.v[2 * i + 1] = mul2(c.v[2 * i + 1], f.v[1]);
+        for (int i = 0; i < VEC / 4; ++i) {
+            const Chunk<float> f = widen_chunk<float>(load16<true>(w + k + 4 * i, any && k < K, 0x3f800000u));
+            c.v[2 * i] = mul2(c.v[2 * i], f.v[0]);
+            c.v[2 * i + 1] = mul2(c.v[2 * i + 1], f.v[1]);
+        }
+    } else {
+        if (!any || k >= K) return;
+        float f[VEC + 4];
+        if (reinterpret_cast<uintptr_t>(w) % 16 == 0) {
+            const int first = k & ~3;
+#pragma unroll
+            for (int i = 0; i < VEC + 4; i += 4) {
+                const uint4 u = load16<true>(w + first + i, first + i >= 0 && first + i < K);
+                f[i] = __uint_as_float(u.x);
+                f[i + 1] = __uint_as_float(u.y);
+                f[i + 2] = __uint_as_float(u.z);
+                f[i + 3] = __uint_as_float(u.w);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC + 2; ++i) f[i] = (k & 2) ? f[i + 2] : f[i];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[i] = (k & 1) ? f[i + 1] : f[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[i] = k + i >= 0 && k + i < K ? w[k + i] : 0.f;
+        }
+        if (!whole<T>(k, K)) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (k + i < 0 || k + i >= K) f[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) c.v[i] = mul2(c.v[i], make_float2(f[2 * i], f[2 * i + 1]));
     }
 }
 
