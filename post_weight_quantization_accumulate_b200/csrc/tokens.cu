@@ -24,7 +24,7 @@
 // B200: tokens of 8192 x 11008 bf16 with values 67 us (6.7 TB/s), without 48
 // (5.6), of a gated activation 77 (5.9; 20 instructions a value); norm of 16384 x
 // 4096 bf16 84 us (6.4 TB/s), with norm and gate after the block 89 (6.0), to
-// tokens 76 (6.2); 16384 x 5003 f16 (rows off their boundaries: shifts) 165 (4.0);
+// tokens 76 (6.2); 16384 x 5003 f16 (rows off their boundaries: shifts) 139 (4.7);
 // one row of 4096 1.9 and 2.9.
 #include "common.cuh"
 
@@ -487,12 +487,10 @@ __device__ __forceinline__ uint32_t pack4(float2 a, float2 b)
 }
 
 // Stores the codes of the chunk at k (elements not there have code 0) and
-// returns their sum.  Called by whole warps; a row's lanes in a warp hold
-// neighbouring chunks.  Off the boundaries of the codes' row a lane stores the
-// word that its chunk shares with the next lane's; at the ends of a row's lanes
-// in the warp, and of the row, single codes.
-template <typename T, bool SHIFT, bool SHORT>
-__device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live, const Chunk<T>& c, const RowThreads<SHORT>& r)
+// returns their sum.  Off the boundaries of the codes' row a whole chunk goes
+// in up to four aligned pieces, the same for all of a row.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live, const Chunk<T>& c)
 {
     constexpr int VEC = kVec<T>;
     uint32_t w[VEC / 4];
@@ -502,35 +500,50 @@ __device__ __forceinline__ int store_codes(int8_t* row, int k, int K, bool live,
         w[j] = pack4(c.v[2 * j], c.v[2 * j + 1]);
         sum = __dp4a(static_cast<int>(w[j]), 0x01010101, sum);
     }
-    if constexpr (!SHIFT) {
-        if (row && live && k < K) {
-            if constexpr (VEC == 8)
-                *reinterpret_cast<uint2*>(row + k) = make_uint2(w[0], w[VEC / 4 - 1]);
-            else
-                *reinterpret_cast<uint32_t*>(row + k) = w[0];
-        }
+    if (!row || !live || k >= K) return sum;
+    if (!SHIFT || (k >= 0 && k % VEC == 0 && k + VEC <= K)) {
+        if constexpr (VEC == 8)
+            *reinterpret_cast<uint2*>(row + k) = make_uint2(w[0], w[VEC / 4 - 1]);
+        else
+            *reinterpret_cast<uint32_t*>(row + k) = w[0];
         return sum;
     }
-    if (!row) return sum;
-    const uint64_t own = VEC == 8 ? static_cast<uint64_t>(w[VEC / 4 - 1]) << 32 | w[0] : w[0];
-    auto put = [&](uint64_t codes, int at, int from, int to) {   // codes[from .. to) at row[at + from ..)
-        if (from == 0 && to == VEC && at >= 0 && at + VEC <= K) {
-            if constexpr (VEC == 8)
-                *reinterpret_cast<uint64_t*>(row + at) = codes;
-            else
-                *reinterpret_cast<uint32_t*>(row + at) = static_cast<uint32_t>(codes);
-        } else {
-            for (int j = from; j < to; ++j)
-                if (at + j >= 0 && at + j < K) row[at + j] = static_cast<int8_t>(codes >> (8 * j));
+    uint64_t codes = VEC == 8 ? static_cast<uint64_t>(w[VEC / 4 - 1]) << 32 | w[0] : w[0];
+    int8_t* p = row + k;
+    if (whole<T>(k, K)) {
+        int left = VEC;
+        if (k & 1) {
+            *p = static_cast<int8_t>(codes);
+            codes >>= 8;
+            p += 1;
+            left -= 1;
         }
-    };
-    const int lead = (VEC - k % VEC) % VEC;   // codes that belong to the word before; the same for a whole row
-    uint64_t next = 0;
-    if (lead) next = __shfl_down_sync(0xffffffffu, own, 1);
-    if (live && k < K) {
-        if (lead && r.lane() == 0) put(own << (8 * (VEC - lead)), k + lead - VEC, VEC - lead, VEC);
-        const uint64_t word = lead ? own >> (8 * lead) | next << (8 * (VEC - lead)) : own;
-        put(word, k + lead, 0, lead && r.lane() == r.width() - 1 ? VEC - lead : VEC);
+        if (reinterpret_cast<uintptr_t>(p) & 2) {
+            *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(codes);
+            codes >>= 16;
+            p += 2;
+            left -= 2;
+        }
+        if (left >= 4) {
+            *reinterpret_cast<uint32_t*>(p) = static_cast<uint32_t>(codes);
+            codes >>= 32;
+            p += 4;
+            left -= 4;
+        }
+        if (left & 4) {   // only where two pieces of 4 follow each other
+            *reinterpret_cast<uint32_t*>(p) = static_cast<uint32_t>(codes);
+            return sum;
+        }
+        if (left & 2) {
+            *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(codes);
+            codes >>= 16;
+            p += 2;
+        }
+        if (left & 1) *p = static_cast<int8_t>(codes);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (k + j >= 0 && k + j < K) p[j] = static_cast<int8_t>(codes >> (8 * j));
     }
     return sum;
 }
@@ -625,7 +638,7 @@ __global__ void __launch_bounds__(THREE ? 384 : kWideThreads, THREE ? 3 : 1) qua
             Chunk<T>& w = v[PACKED ? 0 : i];
             if constexpr (PACKED) w = widen_chunk<T>(xr[i]);
             code_chunk<T, ELEVEN, !GATE && sizeof(T) == 4, decltype(plain)::value>(w, g);
-            sum += store_codes<T, SHIFT>(q, k, a.K, live, w, row);
+            sum += store_codes<T, SHIFT>(q, k, a.K, live, w);
             if (a.hat && live && k < a.K) {
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) w.v[j] = mul2(add2(w.v[j], both(-kRound)), both(g.scale));
@@ -633,8 +646,7 @@ __global__ void __launch_bounds__(THREE ? 384 : kWideThreads, THREE ? 3 : 1) qua
             }
         }
     };
-    // SHORT: the rows of a warp go the same way, for its lanes store together
-    if (SHORT ? __all_sync(0xffffffffu, g.plain()) : g.plain())
+    if (g.plain())
         finish(std::true_type());
     else
         finish(std::false_type());
@@ -736,10 +748,10 @@ __global__ void __launch_bounds__(THREE ? 384 : kWideThreads, THREE ? 3 : 1) blo
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             code_chunk<T, false, false, decltype(plain)::value>(h[i], g);
-            sum += store_codes<T, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i], row);
+            sum += store_codes<T, SHIFT>(a.q + m * a.ldq, k0 + i * step, D, live, h[i]);
         }
     };
-    if (SHORT ? __all_sync(0xffffffffu, g.plain()) : g.plain())
+    if (g.plain())
         finish(std::true_type());
     else
         finish(std::false_type());
