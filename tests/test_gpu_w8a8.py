@@ -5,9 +5,10 @@ Bounds, with u = 2^-24 (half a step of float32) and e = finfo(type).eps / 2
   codes      those of x itself are the exact ones; those of a value v that is
              computed in float32 with a relative error d (and its row's
              maximum too) are within 1/2 + 2 * 127 d of 127 v / t;
-  gate       silu(a) x: exp (2 steps), sum, quotient, product and the
-             subtraction inside exp's argument are below 16 u for the sizes
-             of a used here;
+  gate       silu(a) x: rounding exp's argument costs |a| u, the two
+             approximations and the rest 9 u, which is below 16 u where |a|
+             <= 5; farther out on the negative side |silu| is below 0.04 and
+             falling, and such values are not a row's largest;
   norm       a mean of D squares summed in any order of at most D / 128 + 32
              dependent additions has a relative error of that many u, its
              root half of that; rsqrt, the products with it, the weights and
