@@ -23,19 +23,21 @@
 //  * split kernel: 128 weight rows x NT tokens by a cluster of CTAs that share
 //    K and add their partial sums through distributed shared memory: for few
 //    tokens, where the weights' way from memory is what counts and one tile a
-//    CTA would leave SMs without work.  24 x 11008 x 4096 11.9 us (3.8 TB/s; 7
+//    CTA would leave SMs without work.  24 x 11008 x 4096 10.9 us (4.2 TB/s; 7
 //    of them the weights' bytes, 3.8 a call of one stage).
 //  * few kernel (8 tokens, or a few more of small weights): 16 weight rows a
 //    block, the warps take turns along K and feed mma.sync straight from
 //    global loads.  Nothing but the weights' bytes counts there, and the set-up
 //    of tensor memory, barriers and clusters costs more than the products.
-//    1 x 4096 x 4096 3.6 us (4.7 TB/s), 1 x 28672 x 8192 38.5 us (6.1 TB/s).
+//    1 x 4096 x 4096 3.4 us (5.0 TB/s), 1 x 28672 x 8192 38.5 us (6.1 TB/s).
 //
 // All kernels are programmatic dependent launches: they may start while the
 // kernel before them ends, set themselves up, and wait for its results
-// (pdl_wait) before their first global access.  They let the next kernel start
-// once they hold their tensor memory, never before.  5 to 7% in a chain of such
-// kernels (a decoder layer's, 24 tokens: 63 us against 68).
+// (pdl_wait) before their first global access; for few tokens they ask for their
+// weights to be brought into L2 before that.  They let the next kernel start
+// once they hold their tensor memory, never before.  A decoder layer's chain of
+// such kernels: one token 46 us (50 without the requests), 24 tokens
+// 60 (63 without them, 68 without early starts).
 //
 // The two threads of a CTA that issue loads and MMAs are the elected ones of
 // their warps: under a plain lane test every such instruction took about 110
@@ -190,6 +192,18 @@ __device__ __forceinline__ float output(int acc, const RowScale& r, uint2 t)
 {
     const int sum = static_cast<int>(static_cast<uint32_t>(acc) - r.zero * t.y);
     return __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(sum), r.scale), __uint_as_float(t.x)), r.bias);
+}
+
+// Asks for a box of the weights to be brought into L2, before the kernel before
+// has ended: nothing is read yet, and L2 sees what is written later too.  In the
+// split kernel 24 x 11008 x 4096 in a row 11.2 -> 10.9 us and a layer's chain
+// 63 -> 60, for 5.8 -> 6.3 where a product of 16 MB follows the like of itself; in
+// the pair kernel, with more tokens for each weight, it does not pay (512 x 4096 x
+// 4096 12.8 -> 13.5).
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y)
+                 : "memory");
 }
 
 // ------------------------------------------------------------- pair kernel
@@ -424,6 +438,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         mbar_init(&S.done, 1);
         S.abort = 0;
         fence_mbar_init();
+        for (int k = 0; k < first; ++k) prefetch_box(&mapW, (k_begin + k) * kBK, n0);
         pdl_wait();
         // the first loads are on their way before the block has met
         for (int k = 0; k < first; ++k) load(k, k);
@@ -590,10 +605,17 @@ __device__ __forceinline__ void mma_i8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 }
 
 template <int MT, int U, int W, typename T>
-__global__ void __launch_bounds__(W * 32) w8a8_few_kernel(const W8A8Args a)
+__global__ void __launch_bounds__(W * 32) w8a8_few_kernel(const W8A8Args a, int early)
 {
     __shared__ int part[W][8 * MT][kFewRows];
     pdl_trigger();
+    if (early && threadIdx.x < kFewRows) {   // the block's weights into L2 while the kernel before ends
+        const int64_t r = static_cast<int64_t>(blockIdx.x) * kFewRows + threadIdx.x;
+        if (r < a.N)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.Wq + r * a.ldw),
+                         "r"(static_cast<uint32_t>((a.K + 15) / 16 * 16))
+                         : "memory");
+    }
     pdl_wait();
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -762,9 +784,13 @@ template <int MT, int U, int W, typename T>
 int launch_few(const W8A8Args& a, cudaStream_t stream)
 {
     const unsigned blocks = static_cast<unsigned>((a.N + kFewRows - 1) / kFewRows);
-    // with many small blocks an early start puts more of them on the SMs that
-    // happen to finish first (1 x 11008 x 4096 9.7 us in a row against 9.2)
-    const cudaError_t e = launch_k(w8a8_few_kernel<MT, U, W, T>, dim3(blocks), dim3(W * 32), 0, stream, W == 8, a);
+    // An early start, and the weights asked into L2 meanwhile, where all blocks
+    // are on the SMs at once: gated tokens and 4 x 11008 x 4096 11.0 us against
+    // 11.5, 1 x 4096 x 11008 in a row 8.3 against 10.1.  With more blocks the
+    // first ones' requests only stand in the way of the others' reads (8 x 28672 x
+    // 8192 48 us against 39), and the early start does not matter.
+    const int early = W == 8 || blocks <= 6u * static_cast<unsigned>(sm_count());
+    const cudaError_t e = launch_k(w8a8_few_kernel<MT, U, W, T>, dim3(blocks), dim3(W * 32), 0, stream, early, a, early);
     if (e != cudaSuccess) return cuda_fail(e);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
@@ -836,7 +862,7 @@ int run_typed(const W8A8Args& a, cudaStream_t stream)
     const int64_t weights = a.N * a.K;
     if (a.M <= 8) {
         // many blocks: four warps each and more blocks an SM, whose loads and
-        // reductions overlap (1 x 11008 x 4096 9.1 us against 10.8); else eight
+        // reductions overlap (1 x 11008 x 4096 9.1 us against 10.8 as plain launches); else eight
         // warps a block, each with more on its way (1 x 4096 x 4096 3.6 against 5.2)
         if (a.N >= int64_t(3) * kFewRows * sm_count()) return launch_few<1, 2, 4, T>(a, stream);
         return launch_few<1, 4, 8, T>(a, stream);
