@@ -34,7 +34,7 @@
 // All kernels are programmatic dependent launches: they may start while the
 // kernel before them ends, set themselves up, and wait for its results
 // (pdl_wait) before their first global access; for few tokens they ask for their
-// weights to be brought into L2 before that.  They let the next kernel start
+// first weights to be brought into L2 before that.  They let the next kernel start
 // once they hold their tensor memory, never before.  A decoder layer's chain of
 // such kernels: one token 46 us (50 without the requests), 24 tokens
 // 60 (63 without them, 68 without early starts).
@@ -566,6 +566,12 @@ __global__ void __launch_bounds__(kSplitThreads)
 // same (permuted) order of K on both sides.  A row's 128 codes a step are read
 // in whole lines, U steps in flight a warp.
 constexpr int kFewRows = 16;
+// What a block asks into L2 of each of its weight rows before it waits for the
+// kernel before: enough to bridge that kernel's end, no more, since requests for
+// whole rows stand in the way of the reads themselves.  In a row, of nothing,
+// 2048 and 8192 bytes: 1 x 4096 x 11008 10.0, 9.1, 8.3 us; 1 x 14336 x 4096 10.5,
+// 8.9, 9.9; 1 x 28672 x 8192 37.5, 36.6, 45.3.
+constexpr int64_t kAhead = 2048;
 
 // Not by the read-only path: the kernel may have started before its inputs
 // were there.
@@ -605,16 +611,16 @@ __device__ __forceinline__ void mma_i8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 }
 
 template <int MT, int U, int W, typename T>
-__global__ void __launch_bounds__(W * 32) w8a8_few_kernel(const W8A8Args a, int early)
+__global__ void __launch_bounds__(W * 32) w8a8_few_kernel(const W8A8Args a)
 {
     __shared__ int part[W][8 * MT][kFewRows];
     pdl_trigger();
-    if (early && threadIdx.x < kFewRows) {   // the block's weights into L2 while the kernel before ends
+    if (threadIdx.x < kFewRows) {
         const int64_t r = static_cast<int64_t>(blockIdx.x) * kFewRows + threadIdx.x;
-        if (r < a.N)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.Wq + r * a.ldw),
-                         "r"(static_cast<uint32_t>((a.K + 15) / 16 * 16))
-                         : "memory");
+        if (r < a.N) {
+            const uint32_t bytes = static_cast<uint32_t>(min((a.K + 15) / 16 * 16, kAhead));
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.Wq + r * a.ldw), "r"(bytes) : "memory");
+        }
     }
     pdl_wait();
     const int warp = threadIdx.x >> 5;
@@ -784,13 +790,7 @@ template <int MT, int U, int W, typename T>
 int launch_few(const W8A8Args& a, cudaStream_t stream)
 {
     const unsigned blocks = static_cast<unsigned>((a.N + kFewRows - 1) / kFewRows);
-    // An early start, and the weights asked into L2 meanwhile, where all blocks
-    // are on the SMs at once: gated tokens and 4 x 11008 x 4096 11.0 us against
-    // 11.5, 1 x 4096 x 11008 in a row 8.3 against 10.1.  With more blocks the
-    // first ones' requests only stand in the way of the others' reads (8 x 28672 x
-    // 8192 48 us against 39), and the early start does not matter.
-    const int early = W == 8 || blocks <= 6u * static_cast<unsigned>(sm_count());
-    const cudaError_t e = launch_k(w8a8_few_kernel<MT, U, W, T>, dim3(blocks), dim3(W * 32), 0, stream, early, a, early);
+    const cudaError_t e = launch_k(w8a8_few_kernel<MT, U, W, T>, dim3(blocks), dim3(W * 32), 0, stream, 1, a);
     if (e != cudaSuccess) return cuda_fail(e);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
