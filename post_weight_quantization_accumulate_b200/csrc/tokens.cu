@@ -911,17 +911,21 @@ int launch_rows(void (*kernel)(Args, int), const Args& args, int64_t M, int64_t 
     return GPTQ_OK;
 }
 
-// Chunks a thread: one where there are few rows (the latency of a row counts)
-// or a row is one warp's anyway, else up to four, which keep more bytes on
-// their way a thread and need fewer warps to meet (norm of 16384 x 4096: 91 us
-// with four, 119 with two, 167 with one).  0: one, and part of a warp a row
-// (norm of 500000 x 128: 91 us against 157 with a warp a row).
-template <typename T>
-int chunks_a_thread(int64_t M, int64_t chunks)
+// Chunks a thread, 1, 2 or 4: the fewest from `least` on with which the SMs hold
+// all rows at once (at 64 registers 1024 threads each), since then the latency of
+// a row counts, else `most`, which keep more bytes on their way a thread and need
+// fewer warps to meet (norm of 16384 x 4096: 91 us with four, 119 with two, 167
+// with one; of 444 x 4096 8.8, 6.2, 7.7; of 64 x 4096 5.1, 4.0, 3.7).  0: one, and
+// part of a warp a row (norm of 500000 x 128: 91 us against 157 with a warp a row).
+int chunks_a_thread(int64_t M, int64_t chunks, int least, int most)
 {
     if (chunks <= 16) return 0;
-    if (M <= 2 * sm_count() && chunks <= 1024) return 1;
-    return chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
+    if (chunks <= 32) return 1;
+    for (int n = least; n < most; n *= 2) {
+        const int64_t threads = (chunks + 32 * n - 1) / (32 * n) * 32;
+        if (threads <= kWideThreads && M <= kWideThreads / threads * sm_count()) return n;
+    }
+    return chunks <= 64 ? 2 : most;
 }
 
 template <typename T, bool SHIFT>
@@ -938,7 +942,11 @@ template <typename T, bool SHIFT, bool GATE>
 int tokens_chunked(const TokenArgs& a, cudaStream_t stream)
 {
     const int64_t chunks = chunks_of<T, SHIFT>(a.K);
-    switch (chunks_a_thread<T>(a.M, chunks)) {
+    // Their warps meet once: more warps with a chunk each pay only where a row has
+    // two to four of them, or to eight where each has shifts to do (64 x 4096:
+    // 2.0 us with two chunks, 2.4 with one; 64 x 1003 in float32 2.6 and 2.3).
+    const int least = chunks > 64 && chunks < (SHIFT ? 256 : 129) ? 1 : 2;
+    switch (chunks_a_thread(a.M, chunks, least, 4)) {
         case 0: return launch_rows<1, true>(quantize_tokens_kernel<T, 1, SHIFT, GATE, true>, a, a.M, chunks, stream);
         case 1: return launch_rows<1, false>(quantize_tokens_kernel<T, 1, SHIFT, GATE, false>, a, a.M, chunks, stream);
         case 2: return launch_rows<2, false>(quantize_tokens_kernel<T, 2, SHIFT, GATE, false>, a, a.M, chunks, stream);
@@ -953,7 +961,12 @@ template <typename T, bool SHIFT, bool GATE>
 int norm_chunked(const BlockNormArgs& a, cudaStream_t stream)
 {
     const int64_t chunks = chunks_of<T, SHIFT>(a.D);
-    switch (chunks_a_thread<T>(a.M, chunks)) {
+    // The norm with a gate keeps a third row's chunks: two of each are better for
+    // short rows (8192 x 2048 27 us against 31), and off the boundaries, where
+    // four spill most, while an SM holds three such rows (2048 x 5003 32 us
+    // against 43; but 2048 x 8190 75 against 67).
+    const int most = GATE && chunks <= (SHIFT && sizeof(T) == 2 ? 640 : 256) ? 2 : 4;
+    switch (chunks_a_thread(a.M, chunks, 1, most)) {
         case 0: return launch_rows<1, true>(block_norm_kernel<T, 1, SHIFT, GATE, true>, a, a.M, chunks, stream);
         case 1: return launch_rows<1, false>(block_norm_kernel<T, 1, SHIFT, GATE, false>, a, a.M, chunks, stream);
         case 2: return launch_rows<2, false>(block_norm_kernel<T, 2, SHIFT, GATE, false>, a, a.M, chunks, stream);
