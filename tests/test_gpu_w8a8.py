@@ -185,6 +185,23 @@ def test_tokens_of_a_gated_activation(M, K, t):
     assert torch.equal(hat, (q.float() * s[:, None]).to(t))
 
 
+@pytest.mark.parametrize("M,K,pitch", [(1300, 1000, 1000), (2400, 1000, 1000), (2400, 1001, 1001), (450, 4096, 4096), (700, 4096, 4096),
+                                       (700, 4099, 4100), (20, 11008, 11008), (200, 11008, 11008), (200, 11005, 11005)])
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+def test_tokens_of_few_and_many_rows(M, K, pitch, t):
+    x, a = _randn(M + K, M, K).to(t), (3 * _randn(M + K + 1, M, K)).to(t)
+    q, s, n, hat = _tokens(x, pitch=pitch)
+    assert torch.equal(q.double(), torch.round(_exact_codes(x.double())[0]))
+    assert torch.equal(n.long(), q.long().sum(1))
+    got = w8a8.quantize_tokens(x.cuda(), hat=True)           # rows without a pitch: on 16-byte boundaries where the width allows
+    assert torch.equal(got.codes.cpu(), q) and torch.equal(got.hat.cpu(), hat) and torch.equal(got.sums.cpu(), n)
+    got = w8a8.quantize_tokens(x.cuda(), gate=a.cuda(), hat=True)
+    ratio, top = _exact_codes(a.double() * torch.sigmoid(a.double()) * x.double())
+    d = 16 * U
+    assert ((got.codes.cpu().double() - ratio).abs() <= 0.5 + 2 * 127 * d).all()
+    assert torch.equal(got.hat, (got.codes.float() * got.scales[:, None]).to(t))
+
+
 def test_tokens_of_saturated_gates():
     """silu of gates far out: x for large ones, 0 for far negative ones; an
     infinite negative gate is not a number and marks its row."""
@@ -226,7 +243,7 @@ def _norm_reference(block, residual, pre, post_norm, post, gate, gate_rows, scal
     return r, size, r * rs * w, size * rs * w.abs()
 
 
-def _check_norm(M, D, t, post_norm=True, weights=True, gate_rows=1, scale=0.5, eps=1e-6, parts="br", seed=0, pitch=None):
+def _check_norm(M, D, t, post_norm=True, weights=True, gate_rows=1, scale=0.5, eps=1e-6, parts="br", seed=0, pitch=None, whole=False):
     sd = seed + 31 * M + D
     block = _randn(sd, M, D).to(t) if "b" in parts else None
     residual = (2 * _randn(sd + 1, M, D)).to(t) if "r" in parts else None
@@ -236,8 +253,8 @@ def _check_norm(M, D, t, post_norm=True, weights=True, gate_rows=1, scale=0.5, e
     ld = pitch or D
     dev = lambda a: None if a is None else _pitched(a, ld, 7.0)[:, :D]  # noqa: E731
     vec = lambda a: None if a is None else a.cuda()  # noqa: E731
-    so = torch.full((M + 1, ld + 1), 99.0, dtype=t, device="cuda")
-    out = torch.full((M + 1, ld + 2), 99.0, dtype=t, device="cuda")
+    so = torch.full((M + 1, ld if whole else ld + 1), 99.0, dtype=t, device="cuda")
+    out = torch.full((M + 1, ld if whole else ld + 2), 99.0, dtype=t, device="cuda")
     q = torch.full((M + 1, (D + 15) // 16 * 16 + 16), 99, dtype=torch.int8, device="cuda")
     s, n = torch.full((M + 1,), 99.0, device="cuda"), torch.full((M + 1,), 99, dtype=torch.int32, device="cuda")
     B.gptq_block_norm(dev(block), dev(residual), vec(pre), stream_out=so[:M, :D], out=out[:M, :D], q=q[:M, :D], q_scales=s[:M],
@@ -284,6 +301,16 @@ def test_norm_forms(t, post_norm, weights, gate_rows, parts):
 @pytest.mark.parametrize("pitch", [1001, 1004, 1008, 1024])
 def test_norm_strided_rows(t, pitch):
     _check_norm(7, 1000, t, pitch=pitch)
+
+
+@pytest.mark.parametrize("M,D,whole", [(3, 1000, True), (1300, 1000, True), (2400, 1000, True), (2400, 1001, False), (3, 4096, True),
+                                       (450, 4096, True), (700, 4096, True), (700, 4099, False), (20, 11008, True),
+                                       (200, 11008, True), (200, 11005, False), (9, 64, True), (9, 384, True)])
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+def test_norm_of_few_and_many_rows(M, D, whole, t):
+    """Rows on 16-byte boundaries and off them, few for the SMs and many."""
+    _check_norm(M, D, t, whole=whole)
+    _check_norm(M, D, t, gate_rows=0, whole=whole)
 
 
 def test_norm_scale_and_eps():
