@@ -442,10 +442,13 @@ int gptq_quantize_tokens(int8_t *Xq, int64_t ldq, float *x_scales, int32_t *x_su
  * eps = 0 rows below 1e-19 have none).
  *   stream_out  r' [M, D] OUT or NULL; may be residual itself (lds = ldr).
  *   out         [M, D] OUT or NULL; may be block itself (ldo = ldb).
- *   q           int8 [M, D] OUT or NULL: out as 8-bit tokens, quantized from
- *               its float32 values (as gptq_quantize_tokens; same rules for
- *               rows of zeros and rows that are not finite), with q_scales
- *               float32 [M] and q_sums int32 [M] (or NULL).
+ *   q           int8 [M, D] OUT or NULL: out as 8-bit tokens, of its values
+ *               before they are rounded to `type`, with q_scales float32 [M]
+ *               and q_sums int32 [M] (or NULL).  Each code is that of a value
+ *               within a few roundings of float32 of out: beside a border
+ *               between two codes (2^-15 of a step) it may be either, where
+ *               gptq_quantize_tokens of the same values decides exactly.  Rows
+ *               of zeros and rows that are not finite as there.
  *   block, residual  [M, D]; either may be NULL (then its term is 0), not both.
  *   gate        [n_gates, D] or NULL (1): row m takes gate row m / gate_rows
  *               (gate_rows >= 1; M for one gate of the whole batch).
