@@ -1024,6 +1024,11 @@ int run_block_norm(const BlockNormArgs& a0, int type, cudaStream_t stream)
 {
     BlockNormArgs a = a0;
     a.ahead = 2 * sm_count();
+    if (!a.block) {   // its term is 0, whatever it would be multiplied with
+        a.post_norm = 0;
+        a.post_weight = nullptr;
+        a.gate = nullptr;
+    }
     if (type == GPTQ_F32) return norm_typed<float>(a, stream);
     if (type == GPTQ_F16) return norm_typed<__half>(a, stream);
     return norm_typed<__nv_bfloat16>(a, stream);

@@ -65,3 +65,25 @@ def test_norm_and_product_repeat_their_bits():
             first = tuple(v.clone() for v in got)
         assert all(torch.equal(u, v) for u, v in zip(first, got))
     _done()
+
+
+# -- arguments left out -------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [7, 1000, 1001, 11008, 40000])
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+def test_norm_without_a_block_takes_no_notice_of_its_factors(D, t):
+    """The term of a block that is not there is 0, also where the gate or the
+    weights of the norm after it hold an infinity or NaN: at every row length
+    (those kept in registers, on and off their boundaries, and longer ones)."""
+    r, pre = _randn(D, 6, D).to(t).cuda(), (1 + 0.3 * _randn(D + 1, D)).float().cuda()
+    gate, post = torch.ones(2, D, dtype=t, device="cuda"), torch.ones(D, device="cuda")
+    gate[0, D // 2], gate[1, 0], post[D - 1], post[D // 3] = float("inf"), float("nan"), -float("inf"), float("nan")
+    want = w8a8.block_norm(None, r, pre)
+    wt = w8a8.block_norm(None, r, pre, quantize=True)[1]
+    for scale in (1.0, float("inf")):
+        kw = {"post_norm": True, "post_weight": post, "gate": gate, "gate_rows": 3, "scale": scale}
+        got = w8a8.block_norm(None, r, pre, **kw)
+        t8 = w8a8.block_norm(None, r, pre, quantize=True, **kw)[1]
+        _done()
+        assert torch.equal(got[0], r) and torch.equal(got[1], want[1])
+        assert torch.equal(t8.codes, wt.codes) and torch.equal(t8.scales, wt.scales) and torch.equal(t8.sums, wt.sums)
