@@ -48,6 +48,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 
@@ -713,15 +715,17 @@ int make_map(CUtensorMap* map, const int8_t* p, int64_t cols, int64_t rows, int6
     return GPTQ_OK;
 }
 
-// Raises a kernel's shared-memory limit once per device.
+// Sets a kernel's shared-memory limit, once per device: to the most that any of
+// its launches asks for, so that calls which set it at the same time set the
+// same value and none lowers what another goes by.
 template <typename K>
-int allow_smem(K kernel, int (&done)[64], int bytes)
+int allow_smem(K kernel, std::atomic<bool> (&done)[64], int most)
 {
     int dev = 0;
     GPTQ_CUDA_CHECK(cudaGetDevice(&dev));
-    if (dev < 64 && done[dev] >= bytes) return GPTQ_OK;
-    GPTQ_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-    if (dev < 64) done[dev] = bytes;
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return GPTQ_OK;
+    GPTQ_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
     return GPTQ_OK;
 }
 
@@ -730,7 +734,7 @@ int launch_pair(const W8A8Args& a, cudaStream_t stream)
 {
     constexpr int smem = sizeof(PairSmem<NT>) + 1024;
     static_assert(smem <= 227 * 1024, "one CTA per SM");
-    static int smem_set[64] = {};
+    static std::atomic<bool> smem_set[64] = {};
     int rc = allow_smem(w8a8_pair_kernel<NT, T>, smem_set, smem);
     if (rc) return rc;
     CUtensorMap mapW, mapX;
@@ -756,10 +760,12 @@ int launch_split(const W8A8Args& a, int splits, cudaStream_t stream)
     // all of an SM's shared memory where each has one CTA at most, else half
     // (clusters of more than 4 such CTAs do not all find their SMs in one GPC)
     const bool alone = static_cast<int64_t>(n_tiles) * m_tiles * splits <= sm_count() && splits <= 4;
-    const int stages = std::min({kMaxStages, (alone ? 200 : 104) * 1024 / stage_bytes, (blocks + splits - 1) / splits});
-    const int smem = std::max(stages * stage_bytes, NT * kRows * 4) + 1024;
-    static int smem_set[64] = {};
-    int rc = allow_smem(w8a8_split_kernel<NT, T>, smem_set, smem);
+    constexpr int most_alone = std::min(kMaxStages, 200 * 1024 / stage_bytes), most_shared = std::min(kMaxStages, 104 * 1024 / stage_bytes);
+    const int stages = std::min(alone ? most_alone : most_shared, (blocks + splits - 1) / splits);
+    auto bytes = [](int n) constexpr { return std::max(n * stage_bytes, NT * kRows * 4) + 1024; };
+    const int smem = bytes(stages);
+    static std::atomic<bool> smem_set[64] = {};
+    int rc = allow_smem(w8a8_split_kernel<NT, T>, smem_set, bytes(most_alone));
     if (rc) return rc;
     CUtensorMap mapW, mapX;
     rc = make_map(&mapW, a.Wq, a.K, a.N, a.ldw, kRows);
