@@ -102,6 +102,18 @@ void fake_launch(int i, char* name, int size, long long* v)
     v[5] = l.cluster;
     v[6] = l.early;
 }
+// Compiled kernel i's name, or 0 where there is none.
+int fake_kernel(int i, char* name, int size)
+{
+    std::lock_guard<std::mutex> lk(m);
+    for (auto& [f, k] : kernels())
+        if (i-- == 0) {
+            std::strncpy(name, k.name.c_str(), size - 1);
+            name[size - 1] = 0;
+            return 1;
+        }
+    return 0;
+}
 // How many different values a kernel's limit was set to, the most over all.
 int fake_most_limits()
 {

@@ -6,7 +6,11 @@ import pytest
 import torch
 
 from post_weight_quantization_accumulate_b200 import binding as B
-from post_weight_quantization_accumulate_b200 import w8a8
+from post_weight_quantization_accumulate_b200 import decoder, w8a8
+from post_weight_quantization_accumulate_b200.layer import LayerQuantizer
+
+from test_gpu_w8a8 import _check_product, _norm_reference
+from test_w8a8_launches import PRODUCTS
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +91,127 @@ def test_norm_without_a_block_takes_no_notice_of_its_factors(D, t):
         _done()
         assert torch.equal(got[0], r) and torch.equal(got[1], want[1])
         assert torch.equal(t8.codes, wt.codes) and torch.equal(t8.scales, wt.scales) and torch.equal(t8.sums, wt.sums)
+
+
+# -- the product, every kernel ---------------------------------------------------------
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+def test_product_by_every_kernel(M, N, K, t):
+    """Sizes that are known (test_w8a8_launches) to reach every kernel of the
+    product, its rings of stages and its second and third tiles."""
+    _check_product(M, N, K, t, zeros=True, bias=True, seed=5)
+
+
+# -- the calls that allocate their outputs -----------------------------------------------
+
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+@pytest.mark.parametrize("M,D,gate_rows", [(6, 1000, 4), (37, 1003, 1), (1, 4096, 1), (300, 4096, 300), (2, 40000, 2)])
+def test_block_norm_with_all_of_its_arguments(M, D, gate_rows, t):
+    """Every argument of w8a8.block_norm with values that none of the others
+    could stand for, against the form in 64 bits."""
+    block, residual = _randn(D, M, D).to(t), (2 * _randn(D + 1, M, D)).to(t)
+    pre, post = (1 + 0.3 * _randn(D + 2, D)).float(), (3 + 0.5 * _randn(D + 3, D)).float()
+    gate = (-1.5 + 0.3 * _randn(D + 4, -(-M // gate_rows), D)).to(t)
+    scale, eps = 0.375, 0.25
+    kw = {"post_norm": True, "post_weight": post.cuda(), "gate": gate.cuda(), "gate_rows": gate_rows, "scale": scale, "eps": eps}
+    stream, out = w8a8.block_norm(block.cuda(), residual.cuda(), pre.cuda(), **kw)
+    same, t8 = w8a8.block_norm(block.cuda(), residual.cuda(), pre.cuda(), quantize=True, **kw)
+    only = w8a8.block_norm(block.cuda(), residual.cuda(), pre.cuda(), keep_stream=False, **kw)
+    kept = w8a8.block_norm(block.cuda(), residual.cuda(), pre.cuda(), keep_out=False, **kw)
+    _done()
+    assert only[0] is None and kept[1] is None
+    assert torch.equal(same, stream) and torch.equal(only[1], out) and torch.equal(kept[0], stream)
+    r, size, y, ysize = _norm_reference(block, residual, pre, True, post, gate, gate_rows, scale, eps)
+    d = (D / 128 + 48) * U
+    half, tiny = torch.finfo(t).eps / 2, 2.0 ** -25 if t == F16 else 2.0 ** -130
+    stream, out = stream.cpu().double(), out.cpu().double()
+    assert ((stream - r).abs() <= d * size + half * r.abs() * (1 + d) + d * half * size + tiny).all()
+    assert ((out - y).abs() <= 2 * d * ysize + half * (y.abs() + 2 * d * ysize) + tiny).all()
+    top = y.abs().amax(1, keepdim=True)
+    rsize = 127 * ysize / top
+    codes, scales = t8.codes.cpu().double(), t8.scales.cpu().double()
+    assert ((codes - 127 * y / top).abs() <= 0.5 + 2 * d * (rsize + rsize.amax(1, keepdim=True))).all()
+    assert ((scales - top[:, 0] / 127).abs() <= 2 * d * ysize.amax(1) / 127 + U * top[:, 0] / 127).all()
+    assert torch.equal(t8.sums.cpu().long(), t8.codes.cpu().long().sum(1))
+
+
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+@pytest.mark.parametrize("M,N,K", [(3, 200, 333), (40, 130, 500), (300, 257, 640)])
+def test_linear_with_all_of_its_arguments(M, N, K, t):
+    """w8a8.linear with and without each of bias and zeros."""
+    x = _randn(K, M, K).to(BF16).cuda()
+    tokens = w8a8.quantize_tokens(x)
+    g = torch.Generator().manual_seed(N)
+    codes = w8a8.empty_codes(N, K, "cuda")
+    codes.copy_(torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int32).to(torch.int8))
+    scales, zeros = (torch.rand(N, generator=g) * 1e-3 + 1e-4).cuda(), torch.randint(-128, 128, (N,), generator=g, dtype=torch.int32).cuda()
+    bias = (5 + torch.randn(N, generator=g)).cuda()
+    half, tiny = torch.finfo(t).eps / 2, 2.0 ** -25 if t == F16 else 2.0 ** -130
+    for z in (None, zeros):
+        for b in (None, bias):
+            y = w8a8.linear(tokens, w8a8.Weight(codes, scales, z), bias=b, dtype=t)
+            _done()
+            assert y.dtype == t and y.shape == (M, N) and y.is_contiguous()
+            w = codes.double() - (0 if z is None else z.double()[:, None])
+            p = (tokens.codes.double() @ w.t()) * tokens.scales.double()[:, None] * scales.double()
+            ref = p + (0 if b is None else b.double())
+            bound = 3.01 * U * p.abs() * (1 + half) + (U + half * 1.01) * ref.abs() + tiny
+            assert ((y.double() - ref).abs() <= bound).all()
+
+
+def test_refused_calls_launch_nothing():
+    x = torch.zeros(3, 50, dtype=BF16, device="cuda")
+    t = w8a8.quantize_tokens(x)
+    w = w8a8.Weight(w8a8.empty_codes(7, 50, "cuda").zero_(), torch.ones(7, device="cuda"), torch.zeros(7, dtype=torch.int32, device="cuda"))
+    before = B.gptq_launch_count()
+    for call in (lambda: w8a8.quantize_tokens(x.double()), lambda: w8a8.quantize_tokens(x.t()), lambda: w8a8.quantize_tokens(x, gate=x[:2]),
+                 lambda: w8a8.block_norm(x, x.float()), lambda: w8a8.block_norm(x, x, gate=x[:1], gate_rows=2),
+                 lambda: w8a8.block_norm(x, x, eps=-1.0), lambda: w8a8.linear(t, w, dtype=torch.int8),
+                 lambda: w8a8.linear(w8a8.Tokens(t.codes, t.scales), w), lambda: w8a8.linear(t, w, bias=torch.ones(6, device="cuda")),
+                 lambda: w8a8.linear(t, w8a8.Weight(w.codes.contiguous(), w.scales)),
+                 lambda: w8a8.quantize_tokens(torch.zeros(1, 65537, dtype=BF16, device="cuda"))):
+        with pytest.raises((TypeError, ValueError, B.GptqError)):
+            call()
+    assert B.gptq_launch_count() == before
+    _done()
+
+
+# -- the calibration -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits,gs", [(4, 128), (8, -1)])
+def test_calibration_for_16_bit_inputs(bits, gs):
+    """The decoder layer's calibration, written out from its formulas with the
+    layer quantizer: by default, and with act_bits=16, the codes are the same."""
+    shape = decoder.TINY
+    W, X = decoder.synthetic_layer(shape)
+
+    def rms(x):
+        return (x * torch.rsqrt(x.pow(2).mean(dim=1, keepdim=True) + 1e-6)).to(BF16)
+
+    def quantized(x, names):
+        q = LayerQuantizer(*shape.linear_shape(names[0]), bits, gs, 128, 0.01, False)
+        q.add_batch(x)
+        q.prepare()
+        codes, values = {}, {}
+        for n in names:
+            layer = q.quantize(W[n])
+            codes[n], values[n] = layer.codes.clone(), layer.W_hat.to(BF16)
+        return codes, values
+
+    want, v = quantized(X, ("q", "k", "v"))
+    x_o = rms((X @ v["v"].t()).float())
+    codes, o = quantized(x_o, ("o",))
+    want |= codes
+    x_mlp = rms((X.float() + (x_o @ o["o"].t()).float()).to(BF16).float())
+    codes, gu = quantized(x_mlp, ("gate", "up"))
+    want |= codes
+    x_down = (torch.nn.functional.silu((x_mlp @ gu["gate"].t()).float()) * (x_mlp @ gu["up"].t()).float()).to(BF16)
+    want |= quantized(x_down, ("down",))[0]
+    for kw in ({}, {"act_bits": 16}):
+        res = decoder.calibrate(X, W, shape, bits=bits, group_size=gs, **kw)
+        assert set(res.layers) == set(want) and all(torch.equal(res.layers[n].codes, want[n]) for n in want)
+    # and with 8-bit inputs it is another one
+    res = decoder.calibrate(X, W, shape, bits=bits, group_size=gs, act_bits=8)
+    assert not all(torch.equal(res.layers[n].codes, want[n]) for n in want)
+    _done()

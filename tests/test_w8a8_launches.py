@@ -93,3 +93,40 @@ def test_launches_stay_within_their_limits(lib):
             assert gemm(lib, M, N, K, ty) == 0, (M, N, K)
     assert lib.fake_launches() == 4 * len(sizes)
     assert lib.fake_most_limits() == 1
+
+
+# Products (M, N, K) for every kernel: with rings of stages that go round within a
+# tile, and pairs of CTAs that take three tiles and more.
+PRODUCTS = [(8, 1000, 4096), (5, 7200, 2100), (13, 3000, 5000), (27, 1100, 3500),                      # few tokens
+            (24, 11008, 4096), (24, 20000, 2000), (40, 300, 3000), (24, 4096, 4096),                   # 32 a tile; clusters of 3, 1, 8, 4
+            (100, 4096, 4096), (60, 4096, 4093), (256, 4096, 4096), (130, 3000, 5000),                 # 64 and 128 a tile
+            (200, 4096, 2000), (37, 39990, 1300), (300, 5000, 2000), (150, 20000, 1300),               # pairs, 64 and 128
+            (600, 8200, 1100), (1100, 11000, 1000), (2048, 4096, 4096)]                                # and 256
+
+
+def test_the_listed_products_reach_every_kernel(lib):
+    name, compiled, i = ctypes.create_string_buffer(4096), set(), 0
+    while lib.fake_kernel(i, name, len(name)):
+        m = re.search(r"(w8a8_(?:few|split|pair))_kernel<(.*), float>\(", name.value.decode())
+        compiled |= {m.groups()} if m else set()
+        i += 1
+    reached, laps, turns = set(), set(), set()
+    for M, N, K in PRODUCTS:
+        assert gemm(lib, M, N, K, 2) == 0
+        (kernel, arguments, v), = launches(lib)
+        which = (kernel, arguments.rsplit(", ", 1)[0])
+        reached.add(which)
+        if kernel == "w8a8_few":
+            continue
+        tokens, blocks = int(which[1]), -(-K // 128)
+        if kernel == "w8a8_split":
+            stages, blocks = (v["smem"] - 1024) // (128 * (128 + tokens)), blocks // v["cluster"]
+        else:
+            stages = 192 * 1024 // (128 * (128 + tokens // 2))
+            if -(-N // 256) * -(-M // tokens) > 2 * (v["x"] // 2):
+                turns.add(which)
+        if blocks > stages:
+            laps.add(which)
+    assert len(compiled) == 10 and reached == compiled
+    tiled = {k for k in compiled if k[0] != "w8a8_few"}
+    assert laps == tiled and turns == {k for k in compiled if k[0] == "w8a8_pair"}
