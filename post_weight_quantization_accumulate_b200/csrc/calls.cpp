@@ -192,7 +192,7 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (PyErr_Occurred()) return nullptr;
     need_value(a[5] == Py_None || gate_rows >= 1, "gate_rows must be positive");
     const Rows block = rows(a[0], type, m, d, dev, "block"), residual = rows(a[1], type, m, d, dev, "residual");
-    const Rows gate = rows(a[5], type, gate_rows >= 1 ? (m + gate_rows - 1) / gate_rows : 0, d, dev, "gate");
+    const Rows gate = rows(a[5], type, m > 0 && gate_rows >= 1 ? (m - 1) / gate_rows + 1 : 0, d, dev, "gate");
     const void* pre = vec(a[2], at::kFloat, d, dev, "pre_weight");
     const void* post = vec(a[4], at::kFloat, d, dev, "post_weight");
     const bool quantize = PyObject_IsTrue(a[9]) == 1, keep_out = PyObject_IsTrue(a[11]) == 1;

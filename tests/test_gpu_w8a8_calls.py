@@ -215,3 +215,18 @@ def test_calibration_for_16_bit_inputs(bits, gs):
     res = decoder.calibrate(X, W, shape, bits=bits, group_size=gs, act_bits=8)
     assert not all(torch.equal(res.layers[n].codes, want[n]) for n in want)
     _done()
+
+
+def test_one_gate_row_for_any_number_of_rows():
+    """gate_rows may be larger than the batch, up to the largest 64-bit number;
+    a batch without rows has a gate without rows."""
+    x, r, g = (_randn(k, 5, 64).to(BF16).cuda() for k in range(3))
+    want = w8a8.block_norm(x, r, gate=g[:1], gate_rows=5)
+    for rows in (6, 2 ** 31, 2 ** 63 - 5, 2 ** 63 - 1):
+        got = w8a8.block_norm(x, r, gate=g[:1], gate_rows=rows)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        out = torch.empty_like(x)
+        B.gptq_block_norm(x, r, out=out, gate=g[:1], gate_rows=rows)
+        assert torch.equal(out, want[1])
+        assert w8a8.block_norm(x[:0], r[:0], gate=g[:0], gate_rows=rows)[0].shape == (0, 64)
+    _done()
