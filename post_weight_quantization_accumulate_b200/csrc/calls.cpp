@@ -93,6 +93,7 @@ struct Codes {
     at::Tensor codes, scales, sums;
     Rows rows;
 
+    Codes() = default;
     Codes(int64_t m, int64_t k, at::Device dev, bool with_codes)
     {
         const int64_t pitch = code_pitch(k);
@@ -145,6 +146,13 @@ struct On {
     explicit On(at::Device dev) : guard(dev), stream(c10::cuda::getCurrentCUDAStream(dev.index()).stream()) {}
 };
 
+// Lets other Python threads run while the outputs are allocated and the kernel
+// is launched: both can wait, for memory or for room in the stream's queue.
+struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+};
+
 bool counted(const char* fn, Py_ssize_t got, Py_ssize_t want)
 {
     if (got == want) return true;
@@ -163,14 +171,20 @@ PyObject* quantize_tokens(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int64_t m = x.size(0), k = x.size(1);
     const at::Device dev = x.device();
     const Rows xr = rows(a[0], type, m, k, dev, "x"), gr = rows(a[1], type, m, k, dev, "gate");
-    const On on(dev);
-    const Codes q(m, k, dev, PyObject_IsTrue(a[2]) == 1);
-    const at::Tensor hat = PyObject_IsTrue(a[3]) == 1 ? empty({m, k}, type, dev) : at::Tensor();
-    if (!taken("gptq_quantize_tokens",
-               gptq_quantize_tokens(static_cast<int8_t*>(q.rows.p), q.rows.ld, q.scales.data_ptr<float>(),
-                                    q.sums.data_ptr<int32_t>(), hat.defined() ? hat.data_ptr() : nullptr, k, xr.p, xr.ld, gr.p,
-                                    gr.ld, code, m, k, on.stream)))
-        return nullptr;
+    const bool with_codes = PyObject_IsTrue(a[2]) == 1, with_hat = PyObject_IsTrue(a[3]) == 1;
+    Codes q;
+    at::Tensor hat;
+    int status = 0;
+    {
+        const Released released;
+        const On on(dev);
+        q = Codes(m, k, dev, with_codes);
+        if (with_hat) hat = empty({m, k}, type, dev);
+        status = gptq_quantize_tokens(static_cast<int8_t*>(q.rows.p), q.rows.ld, q.scales.data_ptr<float>(),
+                                      q.sums.data_ptr<int32_t>(), hat.defined() ? hat.data_ptr() : nullptr, k, xr.p, xr.ld, gr.p,
+                                      gr.ld, code, m, k, on.stream);
+    }
+    if (!taken("gptq_quantize_tokens", status)) return nullptr;
     return tuple({q.codes, q.scales, q.sums, hat});
     END_HANDLE_TH_ERRORS
 }
@@ -195,29 +209,28 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
     const Rows gate = rows(a[5], type, m > 0 && gate_rows >= 1 ? (m - 1) / gate_rows + 1 : 0, d, dev, "gate");
     const void* pre = vec(a[2], at::kFloat, d, dev, "pre_weight");
     const void* post = vec(a[4], at::kFloat, d, dev, "post_weight");
-    const bool quantize = PyObject_IsTrue(a[9]) == 1, keep_out = PyObject_IsTrue(a[11]) == 1;
-    const On on(dev);
-    at::Tensor stream, out, codes, scales, sums;
-    Rows q;
-    if (PyObject_IsTrue(a[10]) == 1) stream = empty({m, d}, type, dev);
-    if (keep_out && quantize) {
-        const Codes c(m, d, dev, true);
-        codes = c.codes;
-        scales = c.scales;
-        sums = c.sums;
-        q = c.rows;
-    } else if (keep_out) {
-        out = empty({m, d}, type, dev);
+    const bool post_norm = PyObject_IsTrue(a[3]) == 1, quantize = PyObject_IsTrue(a[9]) == 1;
+    const bool keep_stream = PyObject_IsTrue(a[10]) == 1, keep_out = PyObject_IsTrue(a[11]) == 1;
+    at::Tensor stream, out;
+    Codes q;
+    int status = 0;
+    {
+        const Released released;
+        const On on(dev);
+        if (keep_stream) stream = empty({m, d}, type, dev);
+        if (keep_out && quantize)
+            q = Codes(m, d, dev, true);
+        else if (keep_out)
+            out = empty({m, d}, type, dev);
+        const bool codes = q.codes.defined();
+        status = gptq_block_norm(stream.defined() ? stream.data_ptr() : nullptr, d, out.defined() ? out.data_ptr() : nullptr, d,
+                                 static_cast<int8_t*>(q.rows.p), q.rows.ld, codes ? q.scales.data_ptr<float>() : nullptr,
+                                 codes ? q.sums.data_ptr<int32_t>() : nullptr, block.p, block.ld, residual.p, residual.ld, gate.p,
+                                 gate.ld, gate_rows, static_cast<const float*>(post), static_cast<const float*>(pre), post_norm,
+                                 static_cast<float>(scale), static_cast<float>(eps), code, m, d, on.stream);
     }
-    if (!taken("gptq_block_norm",
-               gptq_block_norm(stream.defined() ? stream.data_ptr() : nullptr, d, out.defined() ? out.data_ptr() : nullptr, d,
-                               static_cast<int8_t*>(q.p), q.ld, q.p ? scales.data_ptr<float>() : nullptr,
-                               q.p ? sums.data_ptr<int32_t>() : nullptr, block.p, block.ld, residual.p, residual.ld, gate.p,
-                               gate.ld, gate_rows, static_cast<const float*>(post), static_cast<const float*>(pre),
-                               PyObject_IsTrue(a[3]) == 1, static_cast<float>(scale), static_cast<float>(eps), code, m, d,
-                               on.stream)))
-        return nullptr;
-    return tuple({stream, out, codes, scales, sums});
+    if (!taken("gptq_block_norm", status)) return nullptr;
+    return tuple({stream, out, q.codes, q.scales, q.sums});
     END_HANDLE_TH_ERRORS
 }
 
@@ -240,14 +253,18 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n)
     const void* ws = vec(a[4], at::kFloat, rows_w, dev, "the weight's scales");
     const void* zeros = vec(a[5], at::kInt, rows_w, dev, "the weight's zeros");
     const void* bias = vec(a[6], at::kFloat, rows_w, dev, "bias");
-    const On on(dev);
-    const at::Tensor y = empty({m, rows_w}, type, dev);
-    if (!taken("gptq_w8a8_gemm",
-               gptq_w8a8_gemm(y.data_ptr(), rows_w, code, static_cast<const int8_t*>(xr.p), xr.ld, static_cast<const float*>(xs),
-                              static_cast<const int32_t*>(sums), static_cast<const int8_t*>(wr.p), wr.ld,
-                              static_cast<const float*>(ws), static_cast<const int32_t*>(zeros), static_cast<const float*>(bias),
-                              m, rows_w, k, on.stream)))
-        return nullptr;
+    at::Tensor y;
+    int status = 0;
+    {
+        const Released released;
+        const On on(dev);
+        y = empty({m, rows_w}, type, dev);
+        status = gptq_w8a8_gemm(y.data_ptr(), rows_w, code, static_cast<const int8_t*>(xr.p), xr.ld, static_cast<const float*>(xs),
+                                static_cast<const int32_t*>(sums), static_cast<const int8_t*>(wr.p), wr.ld,
+                                static_cast<const float*>(ws), static_cast<const int32_t*>(zeros), static_cast<const float*>(bias),
+                                m, rows_w, k, on.stream);
+    }
+    if (!taken("gptq_w8a8_gemm", status)) return nullptr;
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }

@@ -2,6 +2,11 @@
 the device.  Where two calls promise the same values, the bits are compared;
 where a call is compared with a form in 64 bits, the bounds are those derived
 in test_gpu_w8a8."""
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -230,3 +235,51 @@ def test_one_gate_row_for_any_number_of_rows():
         assert torch.equal(out, want[1])
         assert w8a8.block_norm(x[:0], r[:0], gate=g[:0], gate_rows=rows)[0].shape == (0, 64)
     _done()
+
+
+# -- threads ---------------------------------------------------------------------------------
+
+WAITING_LIBRARY = """
+#include <unistd.h>
+#define CALL(name) int name() { usleep(400000); return 0; }
+CALL(gptq_quantize_tokens) CALL(gptq_block_norm) CALL(gptq_w8a8_gemm)
+"""
+
+WATCHED_CALLS = """
+import sys, threading, time
+import torch
+sys.path.insert(0, sys.argv[1])
+import _calls
+x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+q, s = torch.zeros(2, 64, dtype=torch.int8, device="cuda"), torch.ones(2, device="cuda")
+turns, done = 0, False
+def others():
+    global turns
+    while not done:
+        turns += 1
+        time.sleep(0.002)
+thread = threading.Thread(target=others)
+thread.start()
+for call in (lambda: _calls.quantize_tokens(x, None, True, False),
+             lambda: _calls.block_norm(x, x, None, False, None, None, 0, 1.0, 1e-6, False, True, True),
+             lambda: _calls.linear(q, s, None, q, s, None, None, torch.bfloat16)):
+    before = turns
+    call()
+    print(turns - before)
+done = True
+thread.join()
+"""
+
+
+def test_other_threads_run_while_a_call_waits(tmp_path):
+    """A launch can wait for room in the stream's queue.  The calls do not hold
+    the interpreter meanwhile: with a library whose calls take 0.4 s, another
+    thread goes on."""
+    (tmp_path / "wait.c").write_text(WAITING_LIBRARY)
+    subprocess.run(["gcc", "-shared", "-fPIC", str(tmp_path / "wait.c"), "-o", str(tmp_path / "libgptq.so")], check=True)
+    shutil.copy(os.path.join(os.path.dirname(B.__file__), "_calls.so"), tmp_path)
+    run = subprocess.run([sys.executable, "-c", WATCHED_CALLS, str(tmp_path)], capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0, run.stderr
+    turns = [int(v) for v in run.stdout.split()]
+    # of 200 turns in 0.4 s on an idle machine; none while the interpreter is held
+    assert len(turns) == 3 and min(turns) >= 10, turns
