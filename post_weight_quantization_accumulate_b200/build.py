@@ -17,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +26,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgptq.so")
 CALLS = os.path.join(PKG, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS_STAMP = os.path.join(BUILD, "calls.txt")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -54,35 +56,70 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def _calls_for() -> str:
+    """What _calls.so is built for: another torch or Python needs another one."""
+    import torch
+    return f"torch {torch.__version__} python {sys.version}"
+
+
+def calls_up_to_date() -> bool:
+    if not _newer(CALLS, [CALLS_SRC, os.path.join(ROOT, "include", "gptq.h")]) or not os.path.exists(CALLS_STAMP):
+        return False
+    with open(CALLS_STAMP) as f:
+        return f.read() == _calls_for()
+
+
 def build_calls(force: bool = False, verbose: bool = False) -> str:
     """_calls.so: torch's headers and libraries, and libgptq.so beside it."""
-    if not force and _newer(CALLS, [CALLS_SRC, os.path.join(ROOT, "include", "gptq.h")]):
+    if not force and calls_up_to_date():
         return CALLS
     import torch
+    os.makedirs(BUILD, exist_ok=True)
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = CALLS + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
-           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", tmp, "-L", PKG, "-lgptq", "-Wl,-rpath,$ORIGIN",
-           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-           # the C++ runtime that torch has loaded, not a copy of its own: streams of a second,
-           # static one crashed where torch's had set up the locale
-           "-nostdlib++", "-l:libstdc++.so.6", "-Wl,-rpath," + os.path.join(base, "lib")]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    obj = os.path.join(BUILD, f"calls.{os.getpid()}.o")
+    compile_ = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+                "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(base, "include"),
+                "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(cuda, "include"), "-c", CALLS_SRC, "-o", obj]
+    # linked by the C compiler, with the C++ runtime that torch has loaded instead of a copy of its
+    # own: streams of a second, static one crashed where torch's had set up the locale
+    link = [os.environ.get("CC", "gcc"), "-shared", obj, "-o", tmp, "-L", os.path.dirname(LIB), "-lgptq", "-Wl,-rpath,$ORIGIN",
+            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-l:libstdc++.so.6", "-Wl,-rpath," + os.path.join(base, "lib")]
+    try:
+        for cmd in (compile_, link):
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"{cmd[0]} failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALLS)
+    finally:
+        for left in (obj, tmp):
+            if os.path.exists(left):
+                os.remove(left)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(_calls_for())
     return CALLS
+
+
+def _calls_or_warning(force: bool, verbose: bool) -> None:
+    """Only w8a8.py needs _calls.so: where it cannot be built, the library
+    stands by itself, and w8a8 says what is missing when it is called."""
+    try:
+        build_calls(force, verbose)
+    except (RuntimeError, OSError) as e:
+        if os.path.exists(CALLS):
+            os.remove(CALLS)   # of older sources, or for another torch or Python
+        warnings.warn(f"w8a8.py will not work: {e}", RuntimeWarning, stacklevel=3)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and up_to_date():
-        build_calls(force, verbose)
+        _calls_or_warning(force, verbose)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -111,7 +148,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    build_calls(force, verbose)
+    _calls_or_warning(force, verbose)
     return LIB
 
 
