@@ -409,7 +409,8 @@ enum { GPTQ_BF16 = 0, GPTQ_F16 = 1, GPTQ_F32 = 2 };
 
 /*
  * Tokens to 8 bits, one scale a row: v = X or, with a gate, silu(gate) * X
- * (the input of a gated MLP's down projection), in float32;
+ * (the input of a gated MLP's down projection), in float32 (silu of a gate
+ * below -87.3 is 0);
  *     t = max_k |v_k|,  q_k = rint(127 v_k / t),  scale = t / 127,
  *     sum = sum_k q_k,  hat_k = scale * q_k   (ties to even).
  * Without a gate the codes are those of the exact quotients.  A row of zeros

@@ -24,8 +24,10 @@
 // B200: tokens of 8192 x 11008 bf16 with values 67 us (6.7 TB/s), without 48
 // (5.6), of a gated activation 77 (5.9; 20 instructions a value); norm of 16384 x
 // 4096 bf16 84 us (6.4 TB/s), with norm and gate after the block 89 (6.0), to
-// tokens 76 (6.2); 16384 x 5003 f16 (rows off their boundaries: shifts) 139 (4.7);
-// one row of 4096 1.9 and 2.9.
+// tokens 75 (6.2); 8192 x 4096 f32 81 (6.7); 16384 x 5003 f16 139 (4.7: the rows of
+// one tensor and its neighbours lie alike and need no shifts, but every row's float32
+// weights are moved into place, and first and last chunks are partial); one row of
+// 4096 1.9 and 2.9.
 #include "common.cuh"
 
 #include <cuda_bf16.h>
@@ -290,8 +292,8 @@ __device__ __forceinline__ int lead_of(const void* row)
 // ------------------------------------------------------------- reductions
 // silu(a) = a / (1 + exp(-a)).  Rounding -a log2(e) costs exp |a| half steps
 // of float32, the two approximations (2 steps and 1) and the rest 9.  Where
-// exp overflows the reciprocal is 0, and so is silu; an infinite negative a
-// gives NaN.
+// exp(-a) passes 2^126 (a below -87.3) the reciprocal would be subnormal and is 0,
+// and so is silu; an infinite negative a gives NaN.
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
@@ -763,7 +765,9 @@ __global__ void __launch_bounds__(THREE ? 384 : kWideThreads, THREE ? 3 : 1) blo
 }
 
 // -- rows longer than kHeldCols: one block a row, which reads it again (from
-// L2) for each pass over it, element by element
+// L2) for each pass over it, element by element.  Right, not fast: tokens of
+// 2048 x 53248 bf16 122 us (2.7 TB/s), gated 218 (2.5), 2048 x 28672 f32 93
+// (3.2); norm of 2048 x 40000 bf16 645 (1.0), of 2048 x 53248 to tokens 901 (0.8)
 
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) quantize_wide_tokens_kernel(const TokenArgs a)
@@ -898,7 +902,8 @@ bool chunks_ok(const void* p, int64_t ld)
 }
 
 // Launches kernel(args, threads of a row): `chunks` 16-byte pieces a row, CH a
-// thread; blocks of 128 threads at least.
+// thread.  A block has as many rows as fit into 128 threads, one at least: rows of
+// 8, 16, 32 or 64 threads share blocks of 128, one of 96 has a block to itself.
 template <int CH, bool SHORT, typename Args>
 int launch_rows(void (*kernel)(Args, int), const Args& args, int64_t M, int64_t chunks, cudaStream_t stream)
 {

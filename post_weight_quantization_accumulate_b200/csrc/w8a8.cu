@@ -29,7 +29,7 @@
 //    block, the warps take turns along K and feed mma.sync straight from
 //    global loads.  Nothing but the weights' bytes counts there, and the set-up
 //    of tensor memory, barriers and clusters costs more than the products.
-//    1 x 4096 x 4096 3.4 us (5.0 TB/s), 1 x 28672 x 8192 38.5 us (6.1 TB/s).
+//    1 x 4096 x 4096 3.4 us (5.0 TB/s), 1 x 28672 x 8192 36.4 us (6.5 TB/s).
 //
 // All kernels are programmatic dependent launches: they may start while the
 // kernel before them ends, set themselves up, and wait for its results
@@ -37,7 +37,7 @@
 // first weights to be brought into L2 before that.  They let the next kernel start
 // once they hold their tensor memory, never before.  A decoder layer's chain of
 // such kernels: one token 46 us (50 without the requests), 24 tokens
-// 60 (63 without them, 68 without early starts).
+// 59 (63 without them, 68 without early starts).
 //
 // The two threads of a CTA that issue loads and MMAs are the elected ones of
 // their warps: under a plain lane test every such instruction took about 110
@@ -812,7 +812,7 @@ int launch_few(const W8A8Args& a, cudaStream_t stream)
 //   tiles: a start and an end (longer for more tokens a tile and more CTAs than
 //     SMs), then whichever is longest of the issue of a CTA's stages, the operands' way from L2 (14
 //     bytes a ps over all SMs) and the weights' from memory (6.2, less with few CTAs).  128 x 4096 x 4096:
-//     split 128 9.3, split 64 9.7, pair 64 12.9; 256 x 4096 x 11008: split 128
+//     split 128 9.3, split 64 9.7 (which the model takes), pair 64 12.9; 256 x 4096 x 11008: split 128
 //     19.9, pair 128 24.0; 512 x 4096 x 4096: pair 128 14.2, pair 256 17.2,
 //     split 128 16.4; 1024 x 4096 x 4096: pair 256 18.1, pair 128 20.6;
 //     256 x 11008 x 4096: pair 256 19.1, pair 128 22.8, split 128 23.5;

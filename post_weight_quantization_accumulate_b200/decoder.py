@@ -24,7 +24,10 @@ GPTQ path); every GPTQ step runs in libgptq.so through `LayerQuantizer`.
 With `act_bits=8` the calibration is that of an 8-bit linear: each Hessian and
 each product sees the values that the inputs' 8-bit tokens stand for.
 `pack_w8a8` lays out what such a calibration gives (bits=8, group_size=-1) and
-`forward_w8a8` runs the layer with it, in 8-bit tokens and weights.
+`forward_w8a8` runs the layer with it, in 8-bit tokens and weights.  The
+calibration's inputs are rounded to bf16 before they are quantized to tokens,
+the norms and the gated activation of `forward_w8a8` are not: beside a border
+between two codes the two can take different ones.
 """
 from __future__ import annotations
 

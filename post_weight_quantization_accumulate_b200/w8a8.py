@@ -8,7 +8,9 @@ arithmetic happens in libgptq.so; the calls here allocate their outputs, run
 on the current stream of the inputs' device and can be captured into graphs.
 They go through _calls.so, which does in C++ what the gptq_* functions of
 `binding` (for outputs of one's own, in place, or on a stream by argument) do
-in Python.
+in Python; while a call allocates and launches, other Python threads run.
+Nothing here is differentiated: outputs carry no gradient, whatever the inputs
+require, so that what is trained must not pass through these calls.
 """
 from __future__ import annotations
 
@@ -81,7 +83,8 @@ def block_norm(block: torch.Tensor | None, residual: torch.Tensor | None, pre_we
                gate_rows: int = 0, scale: float = 1.0, eps: float = 1e-6, quantize: bool = False, keep_stream: bool = True,
                keep_out: bool = True):
     """(r', out) with r' = residual + scale * gate * norm(block) and out =
-    norm(r'); with `quantize` out is `Tokens`.  Without `keep_stream` r', and
+    norm(r'); with `quantize` out is `Tokens`, of its float32 values up to their
+    rounding (beside a border between two codes either may be taken).  Without `keep_stream` r', and
     without `keep_out` out, is None and not stored.  See gptq_block_norm."""
     r, out, codes, scales, sums = (_native or _calls()).block_norm(
         block, residual, pre_weight, post_norm, post_weight, gate, gate_rows, scale, eps, quantize, keep_stream, keep_out)
