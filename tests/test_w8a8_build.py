@@ -3,6 +3,7 @@ anew, and what is left where it cannot be (with compilers that only write down
 how they were called)."""
 import os
 import stat
+import sys
 import warnings
 
 import pytest
@@ -72,6 +73,12 @@ def test_the_library_stands_where_the_module_cannot_be_built(place):
     with pytest.raises(RuntimeError, match="no torch headers"):
         build_mod.build_calls()
     assert sorted(p.name for p in place[0].iterdir() if p.name.startswith("_calls")) == []
+
+
+def test_the_library_stands_without_torch(place, monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)
+    with pytest.warns(RuntimeWarning, match="torch"):
+        assert build_mod.build() == build_mod.LIB
 
 
 def test_a_built_tree_is_left_alone(place):
