@@ -2,6 +2,7 @@
 the device.  Where two calls promise the same values, the bits are compared;
 where a call is compared with a form in 64 bits, the bounds are those derived
 in test_gpu_w8a8."""
+import math
 import os
 import shutil
 import subprocess
@@ -235,6 +236,23 @@ def test_one_gate_row_for_any_number_of_rows():
         assert torch.equal(out, want[1])
         assert w8a8.block_norm(x[:0], r[:0], gate=g[:0], gate_rows=rows)[0].shape == (0, 64)
     _done()
+
+
+def test_silu_of_gates_around_its_last_value():
+    """exp(87) is below 2^126, exp(88) above: there silu is taken as 0."""
+    a = torch.tensor([[-87.0, -88.0, -88.7, 87.0, 0.0]], device="cuda")
+    x = torch.tensor([[1e30, 1e30, 1e30, -1e-8, 1e30]], device="cuda")
+    for k in (5, 40000):                              # in registers, and element by element
+        g, v = torch.zeros(1, k, device="cuda"), torch.zeros(1, k, device="cuda")
+        g[:, :5], v[:, :5] = a, x
+        t = w8a8.quantize_tokens(v, gate=g)
+        _done()
+        silu = [-87.0 / (1 + math.exp(87.0)), 0.0, 0.0, 87.0, 0.0]
+        want = [s * y for s, y in zip(silu, x[0].double().tolist())]
+        top = max(abs(w) for w in want)
+        assert t.codes[0, :5].tolist() == [round(127 * w / top) for w in want]
+        # 87 log2(e) = 125.5 is rounded by 2^-18 at most, 44 U of its power of 2; log2(e) itself costs 19 U; the rest 9 U
+        assert abs(t.scales.item() - top / 127) <= 100 * U * top / 127
 
 
 # -- threads ---------------------------------------------------------------------------------
